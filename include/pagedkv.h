@@ -446,6 +446,131 @@ pa_status pa_decode_partitions_fp8(void* out, const void* q, const void* k_cache
                                    void* stream);
 
 /*
+ * E4M3 KV cache with a scale per (physical block, kv head) ([P2] "4. 이 밖의
+ * 기법들", quantization; the granularity and the rule below are this library's
+ * reading).  Nothing has to be calibrated: the append finds the scales.
+ *
+ *   k_scales, v_scales  [NB][Hkv] float32 (device, 4-byte aligned): a code of
+ *                 physical block i and kv head h stands for code * scales[i][h]
+ *
+ * pa_reshape_and_cache_fp8_block: for every kv head h and every physical block i
+ * that the call writes (t with slot_mapping[t] / bs = i), keys and values each
+ * on their own:
+ *   a    = max |x[t][h][d]| over the call's tokens of the block, NaNs aside
+ *   need = the smallest power of two 2^e, -40 <= e <= 80, with a <= 448 * 2^e
+ *          (2^80 if none)
+ *   old  = scales[i][h] (0 if that is negative or NaN), or 0 if one of the
+ *          call's slots is the block's first (offset 0): writing it starts the
+ *          block anew
+ *   new  = max(old, need)                                  -> scales[i][h]
+ *   each token's codes: E4M3(fp32(x) / new), as pa_reshape_and_cache_fp8
+ *   if new > old and the block is not started anew, each code at an offset the
+ *   call does not write becomes E4M3(code * (old / new)) (for powers of two
+ *   exact except where it reaches E4M3's subnormals)
+ * Slots of a block started anew that the call does not write keep their bytes.
+ * A negative slot is skipped.  The tokens of one block must stand next to each
+ * other in slot_mapping (pa_seq_append's slots of one sequence after another's
+ * do); two separate runs of one block in a call, or two tokens given the same
+ * slot, race: that block's contents are then unspecified.  One launch.
+ *
+ * pa_decode_fp8_block: pa_decode over such caches, q and out of type `dtype`
+ * (f32 / f16 / bf16), partitions and workspace as pa_decode_fp8.  A scale
+ * outside [2^-40, 2^80] is read as the nearer bound, so one of an all-zero
+ * block may hold 0.  Precision as pa_decode_fp8.
+ *
+ * pa_copy_blocks_fp8_block / pa_swap_blocks_fp8_block: pa_copy_blocks /
+ * pa_swap_blocks of codes and scales in one launch (copy-on-write, forks,
+ * compaction; swap with the host pool's scales in the same kind of memory as
+ * its codes).
+ */
+pa_status pa_reshape_and_cache_fp8_block(const void* key, const void* value, void* k_cache,
+                                         void* v_cache, float* k_scales, float* v_scales,
+                                         const int64_t* slot_mapping, int num_tokens,
+                                         int num_kv_heads, int head_size, int block_size,
+                                         int num_blocks, pa_dtype dtype, void* stream);
+
+pa_status pa_decode_fp8_block(void* out, const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scales, const float* v_scales,
+                              const int32_t* block_tables, int max_blocks_per_seq,
+                              const int32_t* context_lens, int num_seqs, int num_heads,
+                              int num_kv_heads, int head_size, int block_size, int num_blocks,
+                              float scale, pa_dtype dtype, int partition_size,
+                              int max_context_len, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
+pa_status pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                   const int64_t* block_pairs, int num_pairs, int num_kv_heads,
+                                   int head_size, int block_size, int num_blocks, void* stream);
+
+pa_status pa_swap_blocks_fp8_block(void* dst_k_cache, void* dst_v_cache, float* dst_k_scales,
+                                   float* dst_v_scales, int dst_num_blocks,
+                                   const void* src_k_cache, const void* src_v_cache,
+                                   const float* src_k_scales, const float* src_v_scales,
+                                   int src_num_blocks, const int64_t* block_pairs, int num_pairs,
+                                   int num_kv_heads, int head_size, int block_size, void* stream);
+
+/*
+ * Attention under a score rule: models that cap their scores, bias them by
+ * distance or limit what a token sees (the pages treat the plain softmax of
+ * [P1] "자기회귀 생성과 KV 캐시" only; the rule is this library's reading of
+ * common practice).  A query row t at position pos of its sequence (pa_decode's
+ * query: pos = L - 1; pa_decode_multi's query token i: pos = L - Q_b + i) gets
+ *
+ *   s_j  = scale * q . K_j
+ *   s_j  = softcap * tanh(s_j / softcap)             if softcap > 0
+ *   s_j  = s_j - alibi_slopes[h] * |pos - j|         if alibi_slopes
+ *   out  = sum_j softmax_j(s_j) V_j  over first <= j <= last,
+ *   first = max(0, key_starts[t], pos - window + 1)  (window only if > 0)
+ *   last  = max(pos, min(prefix_lens[b], L) - 1)
+ *
+ * and a zero row if nothing is left (first > last).  K/V blocks before the
+ * first position that any query token of a sequence sees are not read.
+ * Whatever positions outside first .. last hold never reaches a row, NaN and
+ * Inf included -- with one exception: in pa_decode_multi_scored a V element that
+ * is not finite, between the first and the last position that some query token
+ * of its sequence sees, may reach all the sequence's query tokens.
+ */
+typedef struct pa_score_rule {
+  float softcap;               /* 0: no cap; else finite and > 0 */
+  int window;                  /* 0: no window; else the number of last positions seen */
+  const float* alibi_slopes;   /* [Hq] float32 (device), or NULL */
+  const int32_t* key_starts;   /* [query rows] int32 (device): the first position of the row's
+                                  document (packed documents), or NULL */
+  const int32_t* prefix_lens;  /* [num_seqs] int32 (device): leading tokens that every token of
+                                  the sequence sees (a prefix attended in both directions),
+                                  or NULL; without effect on a single query */
+} pa_score_rule;
+
+/*
+ * pa_decode and pa_decode_multi under `rule` (host memory; NULL, or a rule with
+ * every field off, is the plain call).  The other arguments, supported types
+ * and shapes, device-side checks and launches are those of the plain calls; the
+ * workspace of pa_decode_workspace_bytes / pa_decode_multi_workspace_bytes for
+ * the same arguments always suffices.  Partitions count from the first block
+ * that a query token sees: with a window the work, the grid and the automatic
+ * partition length follow the window, not the context.  PA_ERR_INVALID for a
+ * softcap that is negative, not finite, or so small that scale / softcap is not
+ * finite, a negative window, or unaligned arrays.
+ */
+pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
+                           const int32_t* block_tables, int max_blocks_per_seq,
+                           const int32_t* context_lens, int num_seqs, int num_heads,
+                           int num_kv_heads, int head_size, int block_size, int num_blocks,
+                           float scale, pa_dtype dtype, const pa_score_rule* rule,
+                           int partition_size, int max_context_len, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+pa_status pa_decode_multi_scored(void* out, const void* q, const void* k_cache,
+                                 const void* v_cache, const int32_t* block_tables,
+                                 int max_blocks_per_seq, const int32_t* context_lens,
+                                 const int32_t* query_start_loc, int num_seqs, int total_q,
+                                 int max_query_len, int num_heads, int num_kv_heads,
+                                 int head_size, int block_size, int num_blocks, float scale,
+                                 pa_dtype dtype, const pa_score_rule* rule, int partition_size,
+                                 int max_context_len, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
+/*
  * Swap ([P1] "적용 범위와 관련 연구": when GPU memory runs short a sequence's KV
  * blocks move to CPU memory and come back later): for each pair p, physical
  * block block_pairs[p][1] of the destination caches becomes a byte copy of

@@ -10,7 +10,7 @@ works but every call raises ``LibraryMissing``: there is no fallback path.
 Layouts (see include/pagedkv.h): q / out [B, Hq, D]; k_cache / v_cache
 [num_blocks, Hkv, block_size, D]; block_tables [B, max_blocks] int32;
 context_lens [B] int32; key / value [N, Hkv, D]; slot_mapping [N] int64;
-block_pairs [P, 2] int64.
+block_pairs [P, 2] int64; k_scales / v_scales [num_blocks, Hkv] float32.
 """
 import ctypes
 import os
@@ -39,7 +39,9 @@ EXPORTS = (
     "pa_seq_free", "pa_seq_move", "pa_seq_num_tokens", "pa_build_tables",
     "pa_alloc_enable_prefix_cache", "pa_alloc_evictable", "pa_seq_add_cached", "pa_seq_commit",
     "pa_decode_grouped", "pa_decode_grouped_fp8", "pa_decode_grouped_workspace_bytes",
-    "pa_build_groups",
+    "pa_build_groups", "pa_reshape_and_cache_fp8_block", "pa_decode_fp8_block",
+    "pa_copy_blocks_fp8_block", "pa_swap_blocks_fp8_block", "pa_decode_scored",
+    "pa_decode_multi_scored",
 )
 
 
@@ -55,6 +57,13 @@ class PagedKVError(RuntimeError):
 
 class OutOfBlocks(PagedKVError):
     pass
+
+
+class _ScoreRule(ctypes.Structure):
+    """pa_score_rule of include/pagedkv.h."""
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int),
+                ("alibi_slopes", ctypes.c_void_p), ("key_starts", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p)]
 
 
 _lib = None
@@ -123,6 +132,18 @@ def lib():
                                    i32, i32, i32, i32, f32, i32, f32, f32, i32, i32, vp, sz, vp],
                                   i32),
         "pa_decode_grouped_workspace_bytes": ([i32, i32, i32, i32, i32, i32], sz),
+        "pa_reshape_and_cache_fp8_block": ([vp, vp, vp, vp, vp, vp, vp, i32, i32, i32, i32, i32,
+                                            i32, vp], i32),
+        "pa_decode_fp8_block": ([vp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32,
+                                 i32, f32, i32, i32, i32, vp, sz, vp], i32),
+        "pa_copy_blocks_fp8_block": ([vp, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp], i32),
+        "pa_swap_blocks_fp8_block": ([vp, vp, vp, vp, i32, vp, vp, vp, vp, i32, vp, i32, i32,
+                                      i32, i32, vp], i32),
+        "pa_decode_scored": ([vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i32, f32,
+                              i32, ctypes.POINTER(_ScoreRule), i32, i32, vp, sz, vp], i32),
+        "pa_decode_multi_scored": ([vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
+                                    i32, i32, i32, f32, i32, ctypes.POINTER(_ScoreRule), i32,
+                                    i32, vp, sz, vp], i32),
         "pa_build_groups": ([pi32, i32, i32, pi32, i32, pi32, pi32, ctypes.POINTER(i32),
                              ctypes.POINTER(i32), ctypes.POINTER(i32)], i32),
     }
@@ -164,6 +185,16 @@ def _contig(*ts):
     for t in ts:
         if t is not None and not t.is_contiguous():
             raise PagedKVError(PA_ERR_INVALID, "tensors must be contiguous")
+
+
+def _current_device(*ts):
+    """Refuses device tensors that are not on the current CUDA device (kernels run
+    there, on its current stream unless one is given)."""
+    import torch
+    for t in ts:
+        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+            raise PagedKVError(PA_ERR_INVALID,
+                               f"tensors must be on the current CUDA device (got {t.device})")
 
 
 # ---------------------------------------------------------------------------
@@ -380,18 +411,117 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale
                                           float(k_scale), float(v_scale), _stream(stream)))
 
 
+def _scales(cache, *scales):
+    """Checks the [num_blocks, Hkv] float32 scales of an E4M3 cache."""
+    import torch
+    for t in scales:
+        if (t.dtype != torch.float32 or tuple(t.shape) != tuple(cache.shape[:2])):
+            raise PagedKVError(PA_ERR_INVALID, "scales must be float32 [num_blocks, Hkv]")
+    _contig(*scales)
+
+
+def pa_decode_fp8_block(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                        scale, max_context_len, partition_size=0, workspace=None,
+                        stream=None) -> None:
+    """pa_decode over E4M3 caches with a scale per (block, kv head): codes of
+    block i and kv head h stand for code * k_scales[i, h] (v_scales for values);
+    q and out f32 / f16 / bf16."""
+    import torch
+    _current_device(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                    workspace)
+    a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
+                     max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
+    _scales(k_cache, k_scales, v_scales)
+    if context_lens.numel() != q.shape[0] or block_tables.shape[0] != q.shape[0]:
+        raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
+    _check(lib().pa_decode_fp8_block(*a[:4], _ptr(k_scales), _ptr(v_scales), *a[4:]))
+
+
+def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping,
+                                   stream=None) -> None:
+    """Store key/value (f32 / f16 / bf16) as E4M3 codes at their slots, finding
+    each block's scale: the smallest power of two that holds the block's largest
+    element, never below the stored one (a block whose first slot is written
+    starts anew); the block's older codes follow when it grows.  The tokens of a
+    block stand next to each other in slot_mapping."""
+    _contig(key, value, k_cache, v_cache, slot_mapping)
+    import torch
+    N, Hkv, D = key.shape
+    NB, Hkv2, bs, D2 = k_cache.shape
+    if (Hkv2, D2) != (Hkv, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
+        raise PagedKVError(PA_ERR_INVALID, "shape mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != N:
+        raise PagedKVError(PA_ERR_INVALID, "slot_mapping must be int64 [N]")
+    if key.dtype != value.dtype or not (k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn):
+        raise PagedKVError(PA_ERR_INVALID, "key/value share a dtype; caches are float8_e4m3fn")
+    _scales(k_cache, k_scales, v_scales)
+    _current_device(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
+    _check(lib().pa_reshape_and_cache_fp8_block(
+        _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+        _ptr(slot_mapping), N, Hkv, D, bs, NB, _dtype_code(key), _stream(stream)))
+
+
+def _scaled_pool(k_cache, v_cache, k_scales, v_scales):
+    import torch
+    _contig(k_cache, v_cache)
+    if v_cache.shape != k_cache.shape:
+        raise PagedKVError(PA_ERR_INVALID, "cache shape mismatch")
+    if not (k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn):
+        raise PagedKVError(PA_ERR_INVALID, "the caches must be float8_e4m3fn")
+    _scales(k_cache, k_scales, v_scales)
+    if k_cache.device.type != "cuda":   # a pool in host memory is read by the GPU
+        for t in (k_cache, v_cache, k_scales, v_scales):
+            if t.device.type != "cpu" or not t.is_pinned():
+                raise PagedKVError(PA_ERR_INVALID, "a host pool must be pinned memory")
+    else:
+        _current_device(k_cache, v_cache, k_scales, v_scales)
+
+
+def _pairs(block_pairs):
+    import torch
+    _contig(block_pairs)
+    if block_pairs.dtype != torch.int64 or (block_pairs.numel() and block_pairs.shape[-1] != 2):
+        raise PagedKVError(PA_ERR_INVALID, "block_pairs must be int64 [P, 2]")
+    return (_ptr(block_pairs) if block_pairs.numel() else None), block_pairs.numel() // 2
+
+
+def pa_copy_blocks_fp8_block(k_cache, v_cache, k_scales, v_scales, block_pairs,
+                             stream=None) -> None:
+    """Block block_pairs[p,1] := block block_pairs[p,0], codes and scales."""
+    _scaled_pool(k_cache, v_cache, k_scales, v_scales)
+    pairs, P = _pairs(block_pairs)
+    NB, Hkv, bs, D = k_cache.shape
+    _check(lib().pa_copy_blocks_fp8_block(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                                          _ptr(v_scales), pairs, P, Hkv, D, bs, NB,
+                                          _stream(stream)))
+
+
+def pa_swap_blocks_fp8_block(dst_k_cache, dst_v_cache, dst_k_scales, dst_v_scales, src_k_cache,
+                             src_v_cache, src_k_scales, src_v_scales, block_pairs,
+                             stream=None) -> None:
+    """pa_swap_blocks for E4M3 caches with a scale per (block, kv head): codes and
+    scales of block block_pairs[p,0] of the source to block_pairs[p,1].  A pool
+    may be pinned host memory (caches and scales)."""
+    _scaled_pool(dst_k_cache, dst_v_cache, dst_k_scales, dst_v_scales)
+    _scaled_pool(src_k_cache, src_v_cache, src_k_scales, src_v_scales)
+    pairs, P = _pairs(block_pairs)
+    NBd, Hkv, bs, D = dst_k_cache.shape
+    if tuple(src_k_cache.shape[1:]) != (Hkv, bs, D):
+        raise PagedKVError(PA_ERR_INVALID, "cache shape mismatch")
+    _check(lib().pa_swap_blocks_fp8_block(
+        _ptr(dst_k_cache), _ptr(dst_v_cache), _ptr(dst_k_scales), _ptr(dst_v_scales), NBd,
+        _ptr(src_k_cache), _ptr(src_v_cache), _ptr(src_k_scales), _ptr(src_v_scales),
+        src_k_cache.shape[0], pairs, P, Hkv, D, bs, _stream(stream)))
+
+
 def pa_decode_multi_workspace_bytes(total_q: int, num_heads: int, head_size: int,
                                     max_context_len: int, partition_size: int = 0) -> int:
     return int(lib().pa_decode_multi_workspace_bytes(total_q, num_heads, head_size,
                                                      max_context_len, partition_size))
 
 
-def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
-                    max_context_len, max_query_len, partition_size=0, workspace=None,
-                    stream=None) -> None:
-    """Several new query tokens per sequence (chunked prefill / speculative
-    verify): q, out [total_q, Hq, D]; query_start_loc int32 [B+1]; sequence b's
-    queries are its last Q_b context tokens, each attending causally."""
+def _multi_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                max_context_len, max_query_len, partition_size, workspace, stream):
     _contig(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace)
     import torch
     T, Hq, D = q.shape
@@ -408,12 +538,81 @@ def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_
     if query_start_loc.numel() != B + 1:
         raise PagedKVError(PA_ERR_INVALID, "query_start_loc must have num_seqs + 1 entries")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().pa_decode_multi(_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache),
-                                 _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
-                                 _ptr(query_start_loc), B, T, int(max_query_len), Hq, Hkv, D, bs,
-                                 NB, float(scale), _dtype_code(q), int(partition_size),
-                                 int(max_context_len), _ptr(workspace), ws_bytes,
-                                 _stream(stream)))
+    return (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
+            block_tables.shape[1], _ptr(context_lens), _ptr(query_start_loc), B, T,
+            int(max_query_len), Hq, Hkv, D, bs, NB, float(scale), _dtype_code(q),
+            int(partition_size), int(max_context_len), _ptr(workspace), ws_bytes,
+            _stream(stream))
+
+
+def pa_decode_multi(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                    max_context_len, max_query_len, partition_size=0, workspace=None,
+                    stream=None) -> None:
+    """Several new query tokens per sequence (chunked prefill / speculative
+    verify): q, out [total_q, Hq, D]; query_start_loc int32 [B+1]; sequence b's
+    queries are its last Q_b context tokens, each attending causally."""
+    _check(lib().pa_decode_multi(*_multi_args(out, q, k_cache, v_cache, block_tables,
+                                              context_lens, query_start_loc, scale,
+                                              max_context_len, max_query_len, partition_size,
+                                              workspace, stream)))
+
+
+class ScoreRule:
+    """What pa_decode_scored / pa_decode_multi_scored do with the scores (pa_score_rule):
+    softcap c > 0: c * tanh(s / c); alibi_slopes float32 [Hq]: - slope * |pos - j|;
+    window w > 0: only the last w positions; key_starts int32 [query rows]: the
+    first position of the row's document; prefix_lens int32 [B]: leading tokens
+    that every query token of the sequence sees.  Tensors on the queries' device."""
+
+    def __init__(self, softcap: float = 0.0, window: int = 0, alibi_slopes=None, key_starts=None,
+                 prefix_lens=None):
+        self.softcap, self.window = float(softcap), int(window)
+        self.alibi_slopes, self.key_starts, self.prefix_lens = alibi_slopes, key_starts, prefix_lens
+
+    def _struct(self, q, num_seqs: int) -> _ScoreRule:
+        import torch
+        rows, heads = q.shape[0], q.shape[1]
+        for name, n, dtype in (("alibi_slopes", heads, torch.float32),
+                               ("key_starts", rows, torch.int32),
+                               ("prefix_lens", num_seqs, torch.int32)):
+            t = getattr(self, name)
+            if t is None:
+                continue
+            if t.dtype != dtype or tuple(t.shape) != (n,) or t.device != q.device:
+                raise PagedKVError(PA_ERR_INVALID,
+                                   f"{name} must be {dtype} [{n}] on the queries' device")
+            _contig(t)
+        return _ScoreRule(self.softcap, self.window, _ptr(self.alibi_slopes),
+                          _ptr(self.key_starts), _ptr(self.prefix_lens))
+
+
+def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale,
+                     max_context_len, rule: ScoreRule, partition_size=0, workspace=None,
+                     stream=None) -> None:
+    """pa_decode under a score rule (capped, distance-biased, windowed scores)."""
+    _current_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
+                     max_context_len, workspace, stream)
+    if context_lens.numel() != q.shape[0] or block_tables.shape[0] != q.shape[0]:
+        raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
+    r = rule._struct(q, q.shape[0])
+    _check(lib().pa_decode_scored(*a[:15], ctypes.byref(r), *a[15:]))
+
+
+def pa_decode_multi_scored(out, q, k_cache, v_cache, block_tables, context_lens,
+                           query_start_loc, scale, max_context_len, max_query_len,
+                           rule: ScoreRule, partition_size=0, workspace=None,
+                           stream=None) -> None:
+    """pa_decode_multi under a score rule, with document starts per query token
+    and prefixes attended in both directions."""
+    _current_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
+                    workspace)
+    a = _multi_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
+                    max_context_len, max_query_len, partition_size, workspace, stream)
+    if block_tables.shape[0] != context_lens.shape[0]:
+        raise PagedKVError(PA_ERR_INVALID, "one table row and length per sequence")
+    r = rule._struct(q, context_lens.shape[0])
+    _check(lib().pa_decode_multi_scored(*a[:18], ctypes.byref(r), *a[18:]))
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, context_lens, scale,

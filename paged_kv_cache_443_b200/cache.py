@@ -21,7 +21,9 @@ from . import (BlockAllocator, Groups, pa_build_groups, pa_copy_blocks, pa_decod
                pa_decode_fp8, pa_decode_grouped, pa_decode_grouped_fp8,
                pa_decode_grouped_workspace_bytes,
                pa_decode_workspace_bytes, pa_reshape_and_cache, pa_reshape_and_cache_fp8,
-               pa_swap_blocks)
+               pa_swap_blocks, ScoreRule, pa_copy_blocks_fp8_block, pa_decode_fp8_block,
+               pa_decode_multi, pa_decode_multi_scored, pa_decode_multi_workspace_bytes,
+               pa_decode_scored, pa_reshape_and_cache_fp8_block, pa_swap_blocks_fp8_block)
 
 
 def _filled(shape, fill: float, dtype: torch.dtype, device) -> torch.Tensor:
@@ -34,17 +36,27 @@ def _filled(shape, fill: float, dtype: torch.dtype, device) -> torch.Tensor:
 class PagedKVCache:
     """dtype: the cache's element type, or torch.float8_e4m3fn for a cache of
     E4M3 codes standing for code * k_scale (keys) and code * v_scale (values);
-    new K/V and queries are then f32 / f16 / bf16 and quantised on append."""
+    new K/V and queries are then f32 / f16 / bf16 and quantised on append.
+    block_scales: the codes have a scale per (block, kv head) instead
+    (self.k_scales, self.v_scales [num_blocks, Hkv] float32), which the append
+    finds; copies and swaps move them with the codes."""
 
     def __init__(self, num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
                  dtype: torch.dtype, device="cuda", initial_free_order: Optional[Sequence[int]] = None,
                  fill: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
-                 prefix_cache: bool = False):
+                 prefix_cache: bool = False, block_scales: bool = False):
         self.num_blocks, self.block_size = num_blocks, block_size
         self.num_kv_heads, self.head_size = num_kv_heads, head_size
         self.dtype, self.device = dtype, torch.device(device)
         self.fp8 = dtype == torch.float8_e4m3fn
         self.k_scale, self.v_scale = float(k_scale), float(v_scale)
+        self.block_scales = block_scales
+        self.k_scales = self.v_scales = self.host_k_scales = self.host_v_scales = None
+        if block_scales:
+            if not self.fp8 or (self.k_scale, self.v_scale) != (1.0, 1.0):
+                raise ValueError("block_scales needs a float8_e4m3fn cache without k_scale / v_scale")
+            self.k_scales = torch.zeros(num_blocks, num_kv_heads, device=self.device)
+            self.v_scales = torch.zeros(num_blocks, num_kv_heads, device=self.device)
         shape = (num_blocks, num_kv_heads, block_size, head_size)
         if fill is None:
             self.k_cache = torch.empty(shape, dtype=dtype, device=self.device)
@@ -99,7 +111,12 @@ class PagedKVCache:
             if not pairs:
                 return
             t = torch.tensor(pairs, dtype=torch.int64, device=self.device)
-        if t.numel():
+        if not t.numel():
+            return
+        if self.block_scales:
+            pa_copy_blocks_fp8_block(self.k_cache, self.v_cache, self.k_scales, self.v_scales, t,
+                                     stream=stream)
+        else:
             pa_copy_blocks(self.k_cache, self.v_cache, t, stream=stream)
 
     def store(self, key: torch.Tensor, value: torch.Tensor, slot_mapping, stream=None) -> None:
@@ -107,7 +124,10 @@ class PagedKVCache:
             slot_mapping = torch.tensor(slot_mapping, dtype=torch.int64, device=self.device)
         if not slot_mapping.numel():
             return
-        if self.fp8:
+        if self.block_scales:
+            pa_reshape_and_cache_fp8_block(key, value, self.k_cache, self.v_cache, self.k_scales,
+                                           self.v_scales, slot_mapping, stream=stream)
+        elif self.fp8:
             pa_reshape_and_cache_fp8(key, value, self.k_cache, self.v_cache, slot_mapping,
                                      self.k_scale, self.v_scale, stream=stream)
         else:
@@ -154,10 +174,16 @@ class PagedKVCache:
     def decode(self, q: torch.Tensor, block_tables: torch.Tensor, context_lens: torch.Tensor,
                max_context_len: int, scale: float, out: Optional[torch.Tensor] = None,
                partition_size: int = 0, workspace: Optional[torch.Tensor] = None,
-               stream=None, groups: Optional[Groups] = None) -> torch.Tensor:
+               stream=None, groups: Optional[Groups] = None,
+               rule: Optional[ScoreRule] = None) -> torch.Tensor:
         """Decode attention of the batch; with `groups` (self.groups(...)) each
         group's shared leading blocks are read once for all its members (the
-        result is the same)."""
+        result is the same); with `rule` the scores follow it (16-bit and f32
+        caches, without groups)."""
+        if rule is not None and (self.fp8 or groups is not None):
+            raise ValueError("a score rule needs a 16-bit or f32 cache and no groups")
+        if groups is not None and self.block_scales:
+            raise ValueError("groups need a cache without block scales")
         if out is None:
             out = torch.empty_like(q)
         if groups is not None:
@@ -176,7 +202,16 @@ class PagedKVCache:
             return out
         if workspace is None:
             workspace = self.workspace(q.shape[0], q.shape[1], max_context_len, partition_size)
-        if self.fp8:
+        if rule is not None:
+            pa_decode_scored(out, q, self.k_cache, self.v_cache, block_tables, context_lens,
+                             scale, max_context_len, rule, partition_size=partition_size,
+                             workspace=workspace, stream=stream)
+        elif self.block_scales:
+            pa_decode_fp8_block(out, q, self.k_cache, self.v_cache, self.k_scales, self.v_scales,
+                                block_tables, context_lens, scale, max_context_len,
+                                partition_size=partition_size, workspace=workspace,
+                                stream=stream)
+        elif self.fp8:
             pa_decode_fp8(out, q, self.k_cache, self.v_cache, block_tables, context_lens, scale,
                           max_context_len, self.k_scale, self.v_scale,
                           partition_size=partition_size, workspace=workspace, stream=stream)
@@ -186,20 +221,57 @@ class PagedKVCache:
                       stream=stream)
         return out
 
+    def decode_multi(self, q: torch.Tensor, block_tables: torch.Tensor,
+                     context_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                     max_context_len: int, max_query_len: int, scale: float,
+                     out: Optional[torch.Tensor] = None, partition_size: int = 0,
+                     workspace: Optional[torch.Tensor] = None, stream=None,
+                     rule: Optional[ScoreRule] = None) -> torch.Tensor:
+        """Several query tokens per sequence (its last tokens, already appended):
+        q [total_q, Hq, D], query_start_loc [B + 1]; 16-bit caches; with `rule`
+        the scores follow it."""
+        if out is None:
+            out = torch.empty_like(q)
+        if workspace is None:
+            n = pa_decode_multi_workspace_bytes(q.shape[0], q.shape[1], self.head_size,
+                                                max_context_len, partition_size)
+            workspace = torch.empty(n // 4, dtype=torch.float32, device=self.device) if n else None
+        args = (out, q, self.k_cache, self.v_cache, block_tables, context_lens, query_start_loc,
+                scale, max_context_len, max_query_len)
+        if rule is not None:
+            pa_decode_multi_scored(*args, rule, partition_size=partition_size,
+                                   workspace=workspace, stream=stream)
+        else:
+            pa_decode_multi(*args, partition_size=partition_size, workspace=workspace,
+                            stream=stream)
+        return out
+
     # ---- swap to / from pinned host memory ----
     def enable_swap(self, num_host_blocks: int) -> None:
         """Pinned host caches of num_host_blocks blocks, with their own block manager."""
         shape = (num_host_blocks, self.num_kv_heads, self.block_size, self.head_size)
         self.host_k = torch.empty(shape, dtype=self.dtype, pin_memory=True)
         self.host_v = torch.empty(shape, dtype=self.dtype, pin_memory=True)
+        if self.block_scales:
+            shape = (num_host_blocks, self.num_kv_heads)
+            self.host_k_scales = torch.zeros(shape, pin_memory=True)
+            self.host_v_scales = torch.zeros(shape, pin_memory=True)
         self.host_alloc = BlockAllocator(num_host_blocks, self.block_size)
+
+    def _pool(self):
+        return self.k_cache, self.v_cache, self.k_scales, self.v_scales
+
+    def _host_pool(self):
+        return self.host_k, self.host_v, self.host_k_scales, self.host_v_scales
 
     def _move(self, src_alloc, dst_alloc, src_caches, dst_caches, seq_ids, stream):
         pairs = src_alloc.move_to(dst_alloc, seq_ids)    # host: sharing kept, all or nothing
         if pairs:
             t = torch.tensor(pairs, dtype=torch.int64, device=self.device)
-            pa_swap_blocks(dst_caches[0], dst_caches[1], src_caches[0], src_caches[1], t,
-                           stream=stream)
+            if self.block_scales:
+                pa_swap_blocks_fp8_block(*dst_caches, *src_caches, t, stream=stream)
+            else:
+                pa_swap_blocks(*dst_caches[:2], *src_caches[:2], t, stream=stream)
         return pairs
 
     def swap_out(self, seq_ids: Sequence[int], stream=None) -> List[Tuple[int, int]]:
@@ -209,13 +281,13 @@ class PagedKVCache:
         released block after the copy."""
         if self.host_alloc is None:
             raise RuntimeError("enable_swap() first")
-        return self._move(self.alloc, self.host_alloc, (self.k_cache, self.v_cache),
-                          (self.host_k, self.host_v), seq_ids, stream)
+        return self._move(self.alloc, self.host_alloc, self._pool(),
+                          self._host_pool(), seq_ids, stream)
 
     def swap_in(self, seq_ids: Sequence[int], stream=None) -> List[Tuple[int, int]]:
         """Bring swapped-out sequences back into fresh device blocks.  Returns the
         (host block, device block) pairs copied; block tables change accordingly."""
         if self.host_alloc is None:
             raise RuntimeError("enable_swap() first")
-        return self._move(self.host_alloc, self.alloc, (self.host_k, self.host_v),
-                          (self.k_cache, self.v_cache), seq_ids, stream)
+        return self._move(self.host_alloc, self.alloc, self._host_pool(),
+                          self._pool(), seq_ids, stream)

@@ -183,6 +183,25 @@ pa_status check_decode_fp8(const char* fn, void* out, const void* q, const void*
   return PA_OK;
 }
 
+// The shape of a cache and its scales, for the calls over block-scaled caches.
+pa_status check_cache_shape(const char* fn, int num_kv_heads, int head_size, int block_size,
+                            int num_blocks) {
+  if (num_kv_heads <= 0 || head_size <= 0 || block_size <= 0 || num_blocks <= 0)
+    return pa::fail(PA_ERR_INVALID, "%s: sizes must be positive", fn);
+  if (!supported_head(head_size))
+    return pa::fail(PA_ERR_UNSUPPORTED, "%s: head_size must be 64 or 128", fn);
+  if (!supported_block(block_size))
+    return pa::fail(PA_ERR_UNSUPPORTED, "%s: block_size must be 8, 16 or 32", fn);
+  return PA_OK;
+}
+
+pa_status check_scales(const char* fn, const float* k_scales, const float* v_scales) {
+  if (!k_scales || !v_scales) return pa::fail(PA_ERR_INVALID, "%s: NULL scales", fn);
+  if ((reinterpret_cast<uintptr_t>(k_scales) & 3u) || (reinterpret_cast<uintptr_t>(v_scales) & 3u))
+    return pa::fail(PA_ERR_INVALID, "%s: k_scales / v_scales must be 4-byte aligned", fn);
+  return PA_OK;
+}
+
 int launch_partitions(const pa::DecodeArgs& a, unsigned int* status, void* stream) {
   if (pa::decode_tc8_supported(a)) return pa::launch_decode_partitions_tc8(a, status, stream);
   if (a.kv_dtype == a.dtype && pa::decode_tc_supported(a)) return pa::launch_decode_partitions_tc(a, status, stream);
@@ -195,6 +214,31 @@ pa_status launch_status(const char* fn, int err, int n_launched) {
                     cudaGetErrorString(static_cast<cudaError_t>(err)));
   pa::count_launch(n_launched);
   return PA_OK;
+}
+
+// pa_copy_blocks_fp8_block (one pool) and pa_swap_blocks_fp8_block (two).
+pa_status copy_scaled(const char* fn, void* dst_k, void* dst_v, float* dst_ks, float* dst_vs,
+                      int dst_blocks, const void* src_k, const void* src_v, const float* src_ks,
+                      const float* src_vs, int src_blocks, const int64_t* pairs, int num_pairs,
+                      int num_kv_heads, int head_size, int block_size, void* stream) {
+  if (num_pairs < 0) return pa::fail(PA_ERR_INVALID, "%s: num_pairs < 0", fn);
+  pa_status st = check_cache_shape(fn, num_kv_heads, head_size, block_size,
+                                   dst_blocks < src_blocks ? dst_blocks : src_blocks);
+  if (st != PA_OK || num_pairs == 0) return st;
+  if (!dst_k || !dst_v || !src_k || !src_v || !pairs)
+    return pa::fail(PA_ERR_INVALID, "%s: NULL pointer", fn);
+  if (!pa::aligned16(dst_k) || !pa::aligned16(dst_v) || !pa::aligned16(src_k) ||
+      !pa::aligned16(src_v) || (reinterpret_cast<uintptr_t>(pairs) & 7u))
+    return pa::fail(PA_ERR_INVALID, "%s: caches must be 16-byte aligned, pairs 8", fn);
+  st = check_scales(fn, dst_ks, dst_vs);
+  if (st == PA_OK) st = check_scales(fn, src_ks, src_vs);
+  if (st != PA_OK) return st;
+  unsigned int* status = pa::device_status_word();
+  if (!status) return PA_ERR_CUDA;
+  const pa::CopyScaled c = {{dst_k, dst_v},   {src_k, src_v}, {dst_ks, dst_vs}, {src_ks, src_vs},
+                            pairs,            num_pairs,      src_blocks,       dst_blocks,
+                            num_kv_heads,     head_size,      block_size};
+  return launch_status(fn, pa::launch_copy_block_scaled(c, status, stream), 1);
 }
 
 }  // namespace
@@ -528,19 +572,47 @@ extern "C" size_t pa_decode_multi_workspace_bytes(int total_q, int num_heads, in
   return workspace_bytes(total_q, num_heads, head_size, num_partitions(max_context_len, P));
 }
 
-extern "C" pa_status pa_decode_multi(void* out, const void* q, const void* k_cache,
-                                     const void* v_cache, const int32_t* block_tables,
-                                     int max_blocks_per_seq, const int32_t* context_lens,
-                                     const int32_t* query_start_loc, int num_seqs, int total_q,
-                                     int max_query_len, int num_heads, int num_kv_heads,
-                                     int head_size, int block_size, int num_blocks, float scale,
-                                     pa_dtype dtype, int partition_size, int max_context_len,
-                                     void* workspace, size_t workspace_bytes_in, void* stream) {
-  const char* fn = "pa_decode_multi";
+namespace {
+
+// Whether a rule changes anything; checks it (PA_OK, or a recorded failure).
+bool rule_active(const pa_score_rule* r) {
+  return r != nullptr && (r->softcap != 0.f || r->window != 0 || r->alibi_slopes != nullptr ||
+                          r->key_starts != nullptr || r->prefix_lens != nullptr);
+}
+
+pa_status check_rule(const char* fn, const pa_score_rule* r, float scale) {
+  if (!std::isfinite(r->softcap) || r->softcap < 0.f)
+    return pa::fail(PA_ERR_INVALID, "%s: softcap must be 0 or finite and > 0", fn);
+  if (r->softcap > 0.f && !std::isfinite(4.f * (scale / r->softcap)))
+    return pa::fail(PA_ERR_INVALID, "%s: softcap is too small for the scale", fn);
+  if (r->window < 0) return pa::fail(PA_ERR_INVALID, "%s: window < 0", fn);
+  if ((reinterpret_cast<uintptr_t>(r->alibi_slopes) & 3u) ||
+      (reinterpret_cast<uintptr_t>(r->key_starts) & 3u) ||
+      (reinterpret_cast<uintptr_t>(r->prefix_lens) & 3u))
+    return pa::fail(PA_ERR_INVALID, "%s: the rule's arrays must be 4-byte aligned", fn);
+  return PA_OK;
+}
+
+// pa_decode_multi, and with a rule pa_decode_multi_scored.
+pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_cache,
+                       const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                       const int32_t* context_lens, const int32_t* query_start_loc, int num_seqs,
+                       int total_q, int max_query_len, int num_heads, int num_kv_heads,
+                       int head_size, int block_size, int num_blocks, float scale, pa_dtype dtype,
+                       const pa_score_rule* rule, int partition_size, int max_context_len,
+                       void* workspace, size_t workspace_bytes_in, void* stream) {
+  // keys that a run of query tokens can span (the whole context without a window)
+  int span = max_context_len;
+  if (rule != nullptr) {
+    const pa_status rs = check_rule(fn, rule, scale);
+    if (rs != PA_OK) return rs;
+    if (max_query_len > 0 && block_size > 0)
+      span = pa::rule_span_bound(*rule, max_context_len, max_query_len, block_size);
+  }
   if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0 && num_heads % num_kv_heads == 0 &&
       max_query_len > 0 && num_seqs >= 0)
     partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len, dtype,
-                                          max_context_len);
+                                          span);
   if (pa::elem_size(dtype) == 0) return pa::fail(PA_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (dtype != PA_F16 && dtype != PA_BF16)
     return pa::fail(PA_ERR_UNSUPPORTED, "%s: q, out and the caches must be f16 or bf16", fn);
@@ -564,7 +636,7 @@ extern "C" pa_status pa_decode_multi(void* out, const void* q, const void* k_cac
   if (total_q > 0 && (max_query_len < 1 || max_query_len > total_q || max_query_len > max_context_len))
     return pa::fail(PA_ERR_INVALID, "%s: max_query_len must be in [1, min(total_q, max_context_len)]", fn);
   if (!std::isfinite(scale)) return pa::fail(PA_ERR_INVALID, "%s: scale is not finite", fn);
-  const int64_t NP = num_partitions(max_context_len, P);
+  const int64_t NP = num_partitions(span, P);
   const int G = num_heads / num_kv_heads;
   const int64_t qblocks = total_q > 0 ? (max_query_len + pa::kMqRows / G - 1) / (pa::kMqRows / G) : 0;
   const int64_t qpairs = (qblocks + pa::kMqTiles - 1) / pa::kMqTiles;
@@ -606,6 +678,8 @@ extern "C" pa_status pa_decode_multi(void* out, const void* q, const void* k_cac
   a.num_partitions = static_cast<int>(NP);
   a.scale = scale;
   a.dtype = dtype;
+  a.has_rule = rule != nullptr;
+  if (rule != nullptr) a.rule = *rule;
   unsigned int* status = pa::device_status_word();
   if (!status) return PA_ERR_CUDA;
   // few queries per sequence: token-major (tokens as the MMA's M, query tokens x
@@ -621,6 +695,171 @@ extern "C" pa_status pa_decode_multi(void* out, const void* q, const void* k_cac
   if (st != PA_OK || NP <= 1) return st;
   return launch_status(fn, pa::launch_decode_mq_reduce(a, stream), 1);
 }
+
+}  // namespace
+
+extern "C" pa_status pa_decode_multi(void* out, const void* q, const void* k_cache,
+                                     const void* v_cache, const int32_t* block_tables,
+                                     int max_blocks_per_seq, const int32_t* context_lens,
+                                     const int32_t* query_start_loc, int num_seqs, int total_q,
+                                     int max_query_len, int num_heads, int num_kv_heads,
+                                     int head_size, int block_size, int num_blocks, float scale,
+                                     pa_dtype dtype, int partition_size, int max_context_len,
+                                     void* workspace, size_t workspace_bytes_in, void* stream) {
+  return decode_multi("pa_decode_multi", out, q, k_cache, v_cache, block_tables,
+                      max_blocks_per_seq, context_lens, query_start_loc, num_seqs, total_q,
+                      max_query_len, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                      scale, dtype, nullptr, partition_size, max_context_len, workspace,
+                      workspace_bytes_in, stream);
+}
+
+extern "C" pa_status pa_decode_multi_scored(void* out, const void* q, const void* k_cache,
+                                            const void* v_cache, const int32_t* block_tables,
+                                            int max_blocks_per_seq, const int32_t* context_lens,
+                                            const int32_t* query_start_loc, int num_seqs,
+                                            int total_q, int max_query_len, int num_heads,
+                                            int num_kv_heads, int head_size, int block_size,
+                                            int num_blocks, float scale, pa_dtype dtype,
+                                            const pa_score_rule* rule, int partition_size,
+                                            int max_context_len, void* workspace,
+                                            size_t workspace_bytes_in, void* stream) {
+  return decode_multi("pa_decode_multi_scored", out, q, k_cache, v_cache, block_tables,
+                      max_blocks_per_seq, context_lens, query_start_loc, num_seqs, total_q,
+                      max_query_len, num_heads, num_kv_heads, head_size, block_size, num_blocks,
+                      scale, dtype, rule_active(rule) ? rule : nullptr, partition_size,
+                      max_context_len, workspace, workspace_bytes_in, stream);
+}
+
+extern "C" pa_status pa_decode_scored(void* out, const void* q, const void* k_cache,
+                                      const void* v_cache, const int32_t* block_tables,
+                                      int max_blocks_per_seq, const int32_t* context_lens,
+                                      int num_seqs, int num_heads, int num_kv_heads,
+                                      int head_size, int block_size, int num_blocks, float scale,
+                                      pa_dtype dtype, const pa_score_rule* rule,
+                                      int partition_size, int max_context_len, void* workspace,
+                                      size_t workspace_bytes_in, void* stream) {
+  const char* fn = "pa_decode_scored";
+  if (!rule_active(rule))
+    return pa_decode(out, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens,
+                     num_seqs, num_heads, num_kv_heads, head_size, block_size, num_blocks, scale,
+                     dtype, partition_size, max_context_len, workspace, workspace_bytes_in,
+                     stream);
+  pa_status st = check_rule(fn, rule, scale);
+  if (st != PA_OK) return st;
+  // the checks see the whole context; the partitions count what a window leaves
+  pa_score_rule seen = *rule;
+  seen.prefix_lens = nullptr;   // the single query is the last token
+  const int span = block_size > 0 && max_context_len > 0
+                       ? pa::rule_span_bound(seen, max_context_len, 1, block_size)
+                       : max_context_len;
+  if (max_blocks_per_seq > 0 && block_size > 0 &&
+      static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+    return pa::fail(PA_ERR_INVALID, "%s: max_context_len %d exceeds max_blocks_per_seq * block_size",
+                    fn, max_context_len);
+  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
+    partition_size = auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, span);
+  pa::DecodeArgs a;
+  st = check_decode_full(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                         context_lens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
+                         num_blocks, scale, dtype, partition_size, span, workspace,
+                         workspace_bytes_in, &a);
+  if (st != PA_OK || num_seqs == 0) return st;
+  a.has_rule = true;
+  a.rule = seen;
+  unsigned int* status = pa::device_status_word();
+  if (!status) return PA_ERR_CUDA;
+  st = launch_status(fn, launch_partitions(a, status, stream), 1);
+  if (st != PA_OK || a.num_partitions <= 1) return st;
+  return launch_status(fn, pa::launch_decode_reduce(a, status, stream), 1);
+}
+
+// ---- E4M3 caches with a scale per (block, kv head) ----
+
+extern "C" pa_status pa_decode_fp8_block(void* out, const void* q, const void* k_cache,
+                                         const void* v_cache, const float* k_scales,
+                                         const float* v_scales, const int32_t* block_tables,
+                                         int max_blocks_per_seq, const int32_t* context_lens,
+                                         int num_seqs, int num_heads, int num_kv_heads,
+                                         int head_size, int block_size, int num_blocks,
+                                         float scale, pa_dtype dtype, int partition_size,
+                                         int max_context_len, void* workspace,
+                                         size_t workspace_bytes_in, void* stream) {
+  const char* fn = "pa_decode_fp8_block";
+  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
+    partition_size =
+        auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, max_context_len);
+  pa::DecodeArgs a;
+  pa_status st = check_decode_fp8(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                                  context_lens, num_seqs, num_heads, num_kv_heads, head_size,
+                                  block_size, num_blocks, scale, dtype, 1.f, 1.f, partition_size,
+                                  max_context_len, workspace, workspace_bytes_in, &a);
+  if (st != PA_OK || num_seqs == 0) return st;
+  st = check_scales(fn, k_scales, v_scales);
+  if (st != PA_OK) return st;
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  unsigned int* status = pa::device_status_word();
+  if (!status) return PA_ERR_CUDA;
+  st = launch_status(fn, launch_partitions(a, status, stream), 1);
+  if (st != PA_OK || a.num_partitions <= 1) return st;
+  return launch_status(fn, pa::launch_decode_reduce(a, status, stream), 1);
+}
+
+extern "C" pa_status pa_reshape_and_cache_fp8_block(const void* key, const void* value,
+                                                    void* k_cache, void* v_cache,
+                                                    float* k_scales, float* v_scales,
+                                                    const int64_t* slot_mapping, int num_tokens,
+                                                    int num_kv_heads, int head_size,
+                                                    int block_size, int num_blocks,
+                                                    pa_dtype dtype, void* stream) {
+  const char* fn = "pa_reshape_and_cache_fp8_block";
+  if (pa::elem_size(dtype) == 0) return pa::fail(PA_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
+  if (dtype == PA_FP8_E4M3)
+    return pa::fail(PA_ERR_INVALID, "%s: key/value must be f32, f16 or bf16", fn);
+  if (num_tokens < 0) return pa::fail(PA_ERR_INVALID, "%s: num_tokens < 0", fn);
+  pa_status st = check_cache_shape(fn, num_kv_heads, head_size, block_size, num_blocks);
+  if (st != PA_OK || num_tokens == 0) return st;
+  if (!key || !value || !k_cache || !v_cache || !slot_mapping)
+    return pa::fail(PA_ERR_INVALID, "%s: NULL device pointer", fn);
+  if (!pa::aligned16(key) || !pa::aligned16(value) || !pa::aligned16(k_cache) ||
+      !pa::aligned16(v_cache) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return pa::fail(PA_ERR_INVALID, "%s: key/value/caches must be 16-byte aligned, slots 8", fn);
+  st = check_scales(fn, k_scales, v_scales);
+  if (st != PA_OK) return st;
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t(1) << 31))
+    return pa::fail(PA_ERR_UNSUPPORTED, "%s: num_tokens * num_kv_heads must be below 2^31", fn);
+  unsigned int* status = pa::device_status_word();
+  if (!status) return PA_ERR_CUDA;
+  return launch_status(fn,
+                       pa::launch_append_block(key, value, k_cache, v_cache, k_scales, v_scales,
+                                               slot_mapping, num_tokens, num_kv_heads, head_size,
+                                               block_size, num_blocks, dtype, status, stream),
+                       1);
+}
+
+extern "C" pa_status pa_swap_blocks_fp8_block(void* dst_k_cache, void* dst_v_cache,
+                                              float* dst_k_scales, float* dst_v_scales,
+                                              int dst_num_blocks, const void* src_k_cache,
+                                              const void* src_v_cache, const float* src_k_scales,
+                                              const float* src_v_scales, int src_num_blocks,
+                                              const int64_t* block_pairs, int num_pairs,
+                                              int num_kv_heads, int head_size, int block_size,
+                                              void* stream) {
+  return copy_scaled("pa_swap_blocks_fp8_block", dst_k_cache, dst_v_cache, dst_k_scales,
+                     dst_v_scales, dst_num_blocks, src_k_cache, src_v_cache, src_k_scales,
+                     src_v_scales, src_num_blocks, block_pairs, num_pairs, num_kv_heads,
+                     head_size, block_size, stream);
+}
+
+extern "C" pa_status pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales,
+                                              float* v_scales, const int64_t* block_pairs,
+                                              int num_pairs, int num_kv_heads, int head_size,
+                                              int block_size, int num_blocks, void* stream) {
+  return copy_scaled("pa_copy_blocks_fp8_block", k_cache, v_cache, k_scales, v_scales, num_blocks,
+                     k_cache, v_cache, k_scales, v_scales, num_blocks, block_pairs, num_pairs,
+                     num_kv_heads, head_size, block_size, stream);
+}
+
 
 // ---- shared-prefix groups ----
 

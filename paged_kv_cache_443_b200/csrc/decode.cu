@@ -50,6 +50,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_rule.cuh"
 
 namespace pa {
 
@@ -218,9 +219,25 @@ struct PartitionParams {
   // by its group (nullable = 0); this launch's partials start at slot_base
   const int32_t* seq_shift;
   int slot_base;
+  // kBlockScales: one scale per (physical block, kv head), [NB][Hkv]
+  const float* k_scales;
+  const float* v_scales;
+  RuleParams rule;  // kScoreRule
 };
 
-template <typename TQ, typename TK, int D, int G, int NCW, int BUDGET, int TPW_>
+// What a partition kernel does besides the plain attention:
+//   kBlockScales  E4M3 codes with a scale per (physical block, kv head).  The
+//     key scale multiplies the token's finished dot; the value scale joins
+//     the score as an added log2, so that P = 2^(s + log2 vs - m) already
+//     weights the raw codes and the running max guards the products p vs,
+//     while the sum of weights adds P / vs: two more FMAs per score and
+//     nothing per cache element;
+//   kScoreRule    capped, distance-biased, windowed scores (pa_rule.cuh): the
+//     sequence is taken from the block of its first visible key on, as if the
+//     tokens before were not there.
+enum Mode { kPlain = 0, kBlockScales = 1, kScoreRule = 2 };
+
+template <typename TQ, typename TK, int D, int G, int NCW, int BUDGET, int TPW_, int MODE = kPlain>
 __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     decode_partition_kernel(const PartitionParams p) {
   using C = Cfg<TK, D, G, NCW, BUDGET, TPW_>;
@@ -259,6 +276,17 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     }
     L -= shift;
   }
+  int first = 0;           // kScoreRule: tokens of the first block before the first visible one
+  if constexpr (MODE == kScoreRule) {
+    int lo, hi;
+    rule_limits(p.rule, b, b, L - 1, L, lo, hi);
+    if (L > 0 && lo > L - 1) L = 0;               // nothing visible: a zero row
+    if (L > 0) {
+      shift = lo / p.block_size * p.block_size;
+      first = lo - shift;
+      L -= shift;
+    }
+  }
   const int64_t grid_cap = static_cast<int64_t>(p.num_partitions - p.slot_base) * P;
   if (L > grid_cap) {
     if (threadIdx.x == 0 && part == 0 && g == 0) atomicOr(p.status, PA_DEVERR_CONTEXT);
@@ -266,7 +294,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
   }
   const int start = part * P;
   if (L == 0) {
-    if (part == 0 && shift == 0) {
+    if (part == 0 && (shift == 0 || MODE == kScoreRule)) {
       TQ* o = static_cast<TQ*>(p.out) + (static_cast<int64_t>(b) * p.Hq + g * G) * D;
       for (int i = threadIdx.x; i < G * D; i += C::THREADS) o[i] = EQ::from_float(0.f);
     }
@@ -275,7 +303,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
   if (start >= L) return;
   const int end = min(L, start + P);
   const int n_tiles = (end - start + C::TOK - 1) / C::TOK;
-  const bool single = (L <= P) && shift == 0;
+  const bool single = (L <= P) && (shift == 0 || MODE == kScoreRule);
 
   if (threadIdx.x == 0) {
 #pragma unroll
@@ -381,9 +409,48 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     for (int e = 0; e < C::EPL; ++e) o[h][e] = 0.f;
   }
 
+  // kBlockScales: in the softmax a lane's scores belong to the warp's token
+  // lane % TPW of the stage; its block's scales are read a stage ahead (and
+  // the block's id two), so the two dependent loads hide behind a stage's copy
+  const int tl = w * C::TPW + lane % C::TPW;
+  int pb_next = -1;
+  float ks_next = 1.f, vs_next = 1.f;
+  auto block_of = [&](int t) -> int {
+    const int j = start + t * C::TOK + tl;
+    return t < n_tiles && j < end
+               ? __ldcg(p.block_tables + static_cast<int64_t>(b) * p.max_blocks + j / p.block_size)
+               : -1;
+  };
+  auto scales_of = [&](int pb) {
+    const bool in = pb >= 0 && pb < p.num_blocks;
+    const int64_t at = static_cast<int64_t>(in ? pb : 0) * p.Hkv + g;
+    ks_next = in ? __ldcg(p.k_scales + at) : 1.f;
+    vs_next = in ? __ldcg(p.v_scales + at) : 1.f;
+  };
+  if constexpr (MODE == kBlockScales) {
+    scales_of(block_of(0));
+    pb_next = block_of(1);
+  }
+  // kScoreRule: the slopes of the CTA's heads, in base 2
+  float slope[MODE == kScoreRule ? G : 1];
+  if constexpr (MODE == kScoreRule) {
+#pragma unroll
+    for (int h = 0; h < G; ++h)
+      slope[h] = p.rule.slopes != nullptr ? __ldcg(p.rule.slopes + g * G + h) * kLog2e : 0.f;
+  }
+
   bool ok = true;
   for (int t = 0; t < n_tiles; ++t) {
     const int s = t % C::S;
+    float ks = 1.f, lvs = 0.f, rvs = 1.f;
+    if constexpr (MODE == kBlockScales) {
+      const float vs = fminf(fmaxf(vs_next, kScaleMin), kScaleMax);
+      ks = fminf(fmaxf(ks_next, kScaleMin), kScaleMax);
+      lvs = __log2f(vs);
+      rvs = __frcp_rn(vs);
+      scales_of(pb_next);
+      pb_next = block_of(t + 2);
+    }
     if (!mbar_wait(&full[s], (t / C::S) & 1, p.status)) {
       ok = false;
       break;
@@ -391,6 +458,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     const TK* Ks = reinterpret_cast<const TK*>(stages + s * C::STAGE_BYTES);
     const TK* Vs = reinterpret_cast<const TK*>(stages + s * C::STAGE_BYTES + C::TILE_BYTES);
     const int n_valid = min(C::TOK, end - (start + t * C::TOK));
+    const int n_first = MODE == kScoreRule ? first - (start + t * C::TOK) : 0;
 
     // ---- scores: partial dots over this lane's chunk, then across the row ----
     float part_dot[C::NV];
@@ -449,6 +517,16 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     for (int ps = 0; ps < C::NPASS; ++ps) {
       const int idx = ps * 32 + lane;
       sv[ps] = idx < C::NSM ? sc[idx] : -INFINITY;
+      if constexpr (MODE == kBlockScales) sv[ps] = fmaf(sv[ps], ks, lvs);
+      if constexpr (MODE == kScoreRule) {
+        const int hh = idx / C::TPW;
+        float sl = 0.f;
+#pragma unroll
+        for (int h = 0; h < G; ++h) sl = (h == hh) ? slope[h] : sl;
+        const float away = static_cast<float>(L - 1 - (start + t * C::TOK + tl));
+        const float x = rule_score(p.rule, sv[ps], sl, away);
+        sv[ps] = idx < C::NSM && tl >= n_first && tl < n_valid ? x : -INFINITY;
+      }
       float x = sv[ps];
 #pragma unroll
       for (int off = C::TPW / 2; off >= 1; off >>= 1) x = fmaxf(x, __shfl_xor_sync(FULL_MASK, x, off));
@@ -476,7 +554,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
       for (int h = 0; h < G; ++h) mh = (h == hh) ? mnew[h] : mh;
       const float pr = (sv[ps] == -INFINITY) ? 0.f : ex2_fast(sv[ps] - mh);
       if (idx < C::NSM) sc[idx] = pr;
-      float x = pr;
+      float x = MODE == kBlockScales ? pr * rvs : pr;
 #pragma unroll
       for (int off = C::TPW / 2; off >= 1; off >>= 1) x += __shfl_xor_sync(FULL_MASK, x, off);
       seg[ps] = x;
@@ -498,7 +576,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     for (int it = 0; it < C::ITERS; ++it) {
       const int row_local = it * C::RPW + r;
       const int row = w * C::TPW + row_local;
-      if (row < n_valid) {
+      if (row < n_valid && (MODE != kScoreRule || row >= n_first)) {
         if constexpr (kMixed) {
           // P rounded to f16 (as the tensor-core kernels round it to the
           // operand type), V exact
@@ -593,6 +671,8 @@ struct ReduceParams {
   const float* ws_l;
   int64_t table_cap;  // tokens a block-table row holds (max_blocks * block_size), or INT64_MAX
   int num_seqs, Hq, partition_size, num_partitions;
+  int block_size;     // kScoreRule
+  RuleParams rule;    // kScoreRule
   // shared-prefix groups: sequence b's first seq_shift[b] tokens were served
   // by its group, whose partials fill slots [0, ceil(shift / P)); the rest of
   // the sequence's partials start at slot_rest (nullable: no groups, 0)
@@ -602,7 +682,7 @@ struct ReduceParams {
 
 // One warp per (sequence, query head) with more than one partition:
 // out = sum_p o_p 2^(m_p - M) / sum_p l_p 2^(m_p - M),  M = max_p m_p.
-template <typename T, int D>
+template <typename T, int D, int MODE = kPlain>
 __global__ void __launch_bounds__(128) decode_reduce_kernel(const ReduceParams p) {
   using E = Elem<T>;
   constexpr int DPL = D / 32;  // dims per lane
@@ -618,6 +698,12 @@ __global__ void __launch_bounds__(128) decode_reduce_kernel(const ReduceParams p
   if (L > p.table_cap) L = static_cast<int>(p.table_cap);
   int S = p.seq_shift ? p.seq_shift[b] : 0;   // tokens its group served
   if (S < 0 || S > L) S = 0;                  // flagged by the partition kernel
+  if constexpr (MODE == kScoreRule) {         // the partition kernel's view of the sequence
+    int lo, hi;
+    rule_limits(p.rule, b, b, L - 1, L, lo, hi);
+    if (lo > L - 1) return;                   // a zero row, written there
+    L -= lo / p.block_size * p.block_size;
+  }
   const int P = p.partition_size;
   int64_t rest = L - S;
   const int64_t cap = static_cast<int64_t>(p.num_partitions - p.slot_rest) * P;
@@ -709,11 +795,11 @@ constexpr int warp_tokens() {
   return (sizeof(TK) == 1 && G <= 2) ? 16 : 8;
 }
 
-template <typename TQ, typename TK, int D, int G, int BUDGET = stage_budget<TK>(), int TPW_ = 8>
+template <typename TQ, typename TK, int D, int G, int BUDGET, int TPW_, int MODE>
 cudaError_t launch_partition_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
   constexpr int NCW = consumer_warps<TK, G>();
   using C = Cfg<TK, D, G, NCW, BUDGET, TPW_>;
-  auto kern = decode_partition_kernel<TQ, TK, D, G, NCW, BUDGET, TPW_>;
+  auto kern = decode_partition_kernel<TQ, TK, D, G, NCW, BUDGET, TPW_, MODE>;
   // opt in to > 48 KB of dynamic shared memory (idempotent, cheap)
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
   if (e != cudaSuccess) return e;
@@ -740,35 +826,45 @@ cudaError_t launch_partition_t(const DecodeArgs& a, unsigned int* status, cudaSt
   p.v_scale = a.v_scale;
   p.seq_shift = a.seq_shift;
   p.slot_base = a.slot_base;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
+  p.rule = make_rule(a.rule, a.scale);
+  if (MODE == kScoreRule) p.scale_log2 = p.rule.scale;
   dim3 grid(a.num_seqs, a.Hkv, a.num_partitions - a.slot_base);
   return launch_overlapped(kern, grid, dim3(C::THREADS), C::SMEM, stream, p);
 }
 
-template <typename TQ, typename TK, int D>
+template <typename TQ, typename TK, int D, int MODE>
 cudaError_t launch_partition_g(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
+  constexpr int B = stage_budget<TK>();
   switch (a.Hq / a.Hkv) {
-    case 1: return launch_partition_t<TQ, TK, D, 1, stage_budget<TK>(), warp_tokens<TK, 1>()>(a, status, stream);
-    case 2: return launch_partition_t<TQ, TK, D, 2, stage_budget<TK>(), warp_tokens<TK, 2>()>(a, status, stream);
-    case 4: return launch_partition_t<TQ, TK, D, 4>(a, status, stream);
-    case 8: return launch_partition_t<TQ, TK, D, 8>(a, status, stream);
+    case 1: return launch_partition_t<TQ, TK, D, 1, B, warp_tokens<TK, 1>(), MODE>(a, status, stream);
+    case 2: return launch_partition_t<TQ, TK, D, 2, B, warp_tokens<TK, 2>(), MODE>(a, status, stream);
+    case 4: return launch_partition_t<TQ, TK, D, 4, B, 8, MODE>(a, status, stream);
+    case 8: return launch_partition_t<TQ, TK, D, 8, B, 8, MODE>(a, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
-template <typename TQ, typename TK>
+template <typename TQ, typename TK, int MODE>
 cudaError_t launch_partition_d(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
   switch (a.D) {
-    case 64: return launch_partition_g<TQ, TK, 64>(a, status, stream);
-    case 128: return launch_partition_g<TQ, TK, 128>(a, status, stream);
+    case 64: return launch_partition_g<TQ, TK, 64, MODE>(a, status, stream);
+    case 128: return launch_partition_g<TQ, TK, 128, MODE>(a, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 template <typename TQ>
 cudaError_t launch_partition_kv(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
-  if (a.kv_dtype == PA_FP8_E4M3) return launch_partition_d<TQ, __nv_fp8_e4m3>(a, status, stream);
+  if (a.kv_dtype == PA_FP8_E4M3) {
+    return a.k_scales != nullptr
+               ? launch_partition_d<TQ, __nv_fp8_e4m3, kBlockScales>(a, status, stream)
+               : launch_partition_d<TQ, __nv_fp8_e4m3, kPlain>(a, status, stream);
+  }
   if (a.kv_dtype != a.dtype) return cudaErrorInvalidValue;
-  return launch_partition_d<TQ, TQ>(a, status, stream);
+  return a.has_rule ? launch_partition_d<TQ, TQ, kScoreRule>(a, status, stream)
+                    : launch_partition_d<TQ, TQ, kPlain>(a, status, stream);
 }
 
 template <typename T>
@@ -787,8 +883,15 @@ cudaError_t launch_reduce_t(const DecodeArgs& a, cudaStream_t stream) {
   p.Hq = a.Hq;
   p.partition_size = a.partition_size;
   p.num_partitions = a.num_partitions;
+  p.block_size = a.block_size;
+  p.rule = make_rule(a.rule, a.scale);
   const int64_t warps = static_cast<int64_t>(a.num_seqs) * a.Hq;
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
+  if (a.has_rule) {
+    return a.D == 64
+               ? launch_overlapped(decode_reduce_kernel<T, 64, kScoreRule>, dim3(grid), dim3(128), 0, stream, p)
+               : launch_overlapped(decode_reduce_kernel<T, 128, kScoreRule>, dim3(grid), dim3(128), 0, stream, p);
+  }
   if (a.D == 64) return launch_overlapped(decode_reduce_kernel<T, 64>, dim3(grid), dim3(128), 0, stream, p);
   return launch_overlapped(decode_reduce_kernel<T, 128>, dim3(grid), dim3(128), 0, stream, p);
 }

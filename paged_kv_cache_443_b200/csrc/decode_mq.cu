@@ -42,6 +42,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_rule.cuh"
 #include "tc_common.cuh"
 
 namespace pa {
@@ -187,6 +188,7 @@ struct MqParams {
   int64_t max_blocks;
   int num_seqs, total_q, Hq, Hkv, num_blocks, block_size, partition_size, num_partitions;
   float scale_log2;
+  RuleParams rule;   // RULE instances (pa_decode_multi_scored)
 };
 
 // Query-major multi-query kernel with two query tiles per CTA: a CTA serves
@@ -201,7 +203,12 @@ struct MqParams {
 // straight from TMEM, so no shared memory holds P.  Warps 0 and 1: producer
 // and MMA issuer; warps 2 + 8X .. 9 + 8X: tile X.  Shared memory: the K/V ring
 // and the two Q tiles (~167 KB); all 512 TMEM columns.
-template <typename T, int G>
+// RULE: capped, distance-biased, windowed scores (pa_rule.cuh).  The CTA's keys
+// run from the block of the first key that any of its query tokens sees
+// (positions below are counted from there) to the last one; the first pass
+// over a tile's scores applies the rule and leaves the finished scores in TMEM
+// for the second.
+template <typename T, int G, bool RULE = false>
 __global__ void __launch_bounds__(THREADS2, 1)
     decode_mq_kernel(const MqParams p, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
@@ -236,7 +243,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int P = p.partition_size;
   int64_t cap = p.max_blocks * p.block_size;
   const int64_t grid_cap = static_cast<int64_t>(p.num_partitions) * P;
-  cap = cap < grid_cap ? cap : grid_cap;
+  if (!RULE) cap = cap < grid_cap ? cap : grid_cap;
   if (L < 0 || L > cap || Qb < 0 || Qb > L || q0 < 0 || q0 + Qb > p.total_q) {
     if (threadIdx.x == 0 && pair == 0 && part == 0 && g == 0) atomicOr(p.status, PA_DEVERR_CONTEXT);
     return;
@@ -246,7 +253,29 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int qb0 = pair * NT;                        // the CTA's first query block
   if (qb0 * QB >= Qb) return;                       // no query tokens here
   const int i_last = min(Qb, (qb0 + NT) * QB) - 1;  // the CTA's last query token
-  const int pmax = L - Qb + i_last;                 // its position: the last key needed
+  int pmax = L - Qb + i_last;                       // its position: the last key needed
+  int shift = 0, first = 0;   // RULE: tokens before the first key's block, and from there to it
+  if constexpr (RULE) {
+    int lo, hi;
+    rule_span(p.rule, b, q0, L - Qb, L, qb0 * QB, i_last + 1, lo, hi);
+    if (lo > hi) {                                  // nothing is seen: zero rows
+      if (part == 0) {
+        const int i0 = qb0 * QB;
+        for (int i = threadIdx.x; i < (i_last + 1 - i0) * G * DH; i += THREADS2) {
+          const int64_t hq = (static_cast<int64_t>(q0) + i0 + i / (G * DH)) * p.Hq + g * G + i / DH % G;
+          static_cast<T*>(p.out)[hq * DH + i % DH] = Elem<T>::from_float(0.f);
+        }
+      }
+      return;
+    }
+    shift = lo / p.block_size * p.block_size;
+    first = lo - shift;
+    pmax = hi - shift;
+    if (pmax >= grid_cap) {                         // a context beyond max_context_len
+      if (threadIdx.x == 0 && part == 0 && g == 0) atomicOr(p.status, PA_DEVERR_CONTEXT);
+      return;
+    }
+  }
   const int kstart = part * P;
   if (kstart > pmax) return;
   const int kend = min(kstart + P, pmax + 1);
@@ -257,7 +286,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int bpt = TOK / bs;
   const int first_blk = kstart / bs;
   const int last_blk = (kend + bs - 1) / bs;
-  const int32_t* trow = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
+  const int32_t* trow = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + shift / bs;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&ring_full[s], 1);
@@ -338,7 +367,18 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int qtok = (qb0 + X) * QB + il;             // query token of the row within the sequence
   const bool row_valid = warp >= 2 && qtok < Qb;
   const int64_t t = static_cast<int64_t>(q0) + qtok;
-  const int pos = L - Qb + qtok;
+  const int pos = L - Qb + qtok - shift;
+  // RULE: the keys that the row sees, and its head's slope in base 2
+  int row_lo = 0, row_hi = -1;
+  float slope = 0.f;
+  if constexpr (RULE) {
+    if (row_valid) {
+      rule_limits(p.rule, b, t, L - Qb + qtok, L, row_lo, row_hi);
+      row_lo -= shift;
+      row_hi -= shift;
+      if (p.rule.slopes != nullptr) slope = __ldcg(p.rule.slopes + g * G + hl) * kLog2e;
+    }
+  }
   const int pair_bar = 3 + X * 4 + quad;            // named barrier of this row's two threads
 
   if (warp >= 2) {
@@ -443,8 +483,10 @@ __global__ void __launch_bounds__(THREADS2, 1)
       wait(&s_full[X], i & 1);
       tc_fence_after();
       if (warp_active) {
-        const int lim = row_valid ? min(pos - tile0, n_valid - 1) : -1;  // last key column
-        const bool open = __all_sync(FULL, col0 + 63 <= lim);
+        const int lim =   // last key column
+            RULE ? min(row_hi - tile0, n_valid - 1) : row_valid ? min(pos - tile0, n_valid - 1) : -1;
+        const int lo_c = RULE ? row_lo - tile0 : 0;                      // first key column
+        const bool open = __all_sync(FULL, col0 + 63 <= lim && (!RULE || col0 >= lo_c));
         // pass 1: the row's maximum over this half (raw scores when open)
         float pm[8];
 #pragma unroll
@@ -456,6 +498,19 @@ __global__ void __launch_bounds__(THREADS2, 1)
           else
 #pragma unroll
             for (int j = 0; j < 32; ++j) sv[j] = 0.f;
+          if constexpr (RULE) {
+            const float d0 = static_cast<float>(pos - tile0 - col0 - c * 32);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = col0 + c * 32 + j;
+              const float x =
+                  rule_score(p.rule, sv[j] * p.scale_log2, slope, fabsf(d0 - static_cast<float>(j)));
+              sv[j] = open || (col >= lo_c && col <= lim) ? x : -INFINITY;
+              pm[j & 7] = fmaxf(pm[j & 7], sv[j]);
+            }
+            tmem_st32(s_col + c * 32, sv);
+            continue;
+          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float x = open ? sv[j] : (col0 + c * 32 + j <= lim ? sv[j] : -INFINITY);
@@ -464,7 +519,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
         }
         float tmax = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
                            fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-        tmax = tmax == -INFINITY ? tmax : tmax * p.scale_log2;
+        if (!RULE) tmax = tmax == -INFINITY ? tmax : tmax * p.scale_log2;
         rmax[(((i & 1) * NT + X) * 2 + half) * MR + r] = tmax;
         named_sync(pair_bar, 64);
         tmax = fmaxf(tmax, rmax[(((i & 1) * NT + X) * 2 + (half ^ 1)) * MR + r]);
@@ -488,7 +543,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
           }
         }
         // pass 2: P = 2^(scale * s - m) into the first 32 of my S columns
-        const float neg_m = -m_run;
+        const float neg_m = RULE && m_run == -INFINITY ? 0.f : -m_run;
         float ps[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) ps[k] = 0.f;
@@ -504,7 +559,10 @@ __global__ void __launch_bounds__(THREADS2, 1)
           for (int e = 0; e < 16; ++e) {
             const int j0 = 2 * e, j1 = 2 * e + 1;
             float p0, p1;
-            if (open) {
+            if (RULE) {
+              p0 = ex2_approx(sv[j0] + neg_m);      // masked: 2^-inf = 0
+              p1 = ex2_approx(sv[j1] + neg_m);
+            } else if (open) {
               p0 = ex2_approx(fmaf(sv[j0], p.scale_log2, neg_m));
               p1 = ex2_approx(fmaf(sv[j1], p.scale_log2, neg_m));
             } else {
@@ -528,11 +586,12 @@ __global__ void __launch_bounds__(THREADS2, 1)
         tmem_st16u(s_col, z);
         tmem_st16u(s_col + 16, z);
       }
-      if (X == 0 && n_valid < TOK) {
+      const int n_first = RULE ? first - tile0 : 0;   // > 0 in the first tile only
+      if (X == 0 && (n_valid < TOK || (RULE && n_first > 0))) {
         // the last tile: zero the V rows of keys past the range (this thread
         // its 64-dim half of row r), so that whatever they hold adds 0 to O
         const int u = 2 * i + 1, s_ = u % SLOTS;
-        if (wait(&ring_full[s_], (u / SLOTS) & 1) && r >= n_valid) {
+        if (wait(&ring_full[s_], (u / SLOTS) & 1) && (r >= n_valid || (RULE && r < n_first))) {
           uint8_t* row = ring + s_ * SLOT_BYTES + (r >> 3) * GROUP_BYTES + (r & 7) * 128 + half * HALF_OFF;
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0, 0, 0, 0);
@@ -557,7 +616,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
       tmem_ld32(o_col + c * 32, o);
       if (ok && row_valid) {
         if (single) {
-          const float inv = 1.f / l_sum;
+          const float inv = RULE && l_sum == 0.f ? 0.f : 1.f / l_sum;
           T* dst = static_cast<T*>(p.out) + hq * DH + col0 + c * 32;
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
@@ -601,10 +660,12 @@ struct MqReduceParams {
   const float* ws_l;
   int num_seqs, total_q, Hq, partition_size, num_partitions;
   int direct_qblock;  // query-token run length of the partition launcher (MqArgs)
+  int block_size;     // RULE
+  RuleParams rule;    // RULE
 };
 
 // One warp per (query token, head) whose block spanned several partitions.
-template <typename T>
+template <typename T, bool RULE = false>
 __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReduceParams p) {
   constexpr int DPL = DH / 32;
   grid_dependency_wait();
@@ -627,9 +688,17 @@ __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReducePar
   // grouping), and that run's last key position
   const int QB = p.direct_qblock;
   const int i_last = min(Qb, (i / QB + 1) * QB) - 1;
-  const int pmax = L - Qb + i_last;
+  int pmax = L - Qb + i_last;
+  int pos = L - Qb + i;
+  if constexpr (RULE) {
+    // the run's keys as the partition kernel took them; a partition that this
+    // token sees nothing of holds a partial of max -inf
+    int lo, hi;
+    rule_span(p.rule, b, p.query_start[b], L - Qb, L, i / QB * QB, i_last + 1, lo, hi);
+    if (lo > hi) return;                            // zero rows, written there
+    pmax = pos = hi - lo / p.block_size * p.block_size;
+  }
   if (pmax < p.partition_size) return;              // written directly
-  const int pos = L - Qb + i;
   const int np = min(pos / p.partition_size + 1, p.num_partitions);
   const int64_t base = row * p.num_partitions;
   float M = -INFINITY;
@@ -637,6 +706,7 @@ __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReducePar
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(FULL, M, off));
   float Ls = 0.f;
+  if (RULE && M == -INFINITY) M = 0.f;              // this token sees nothing
   for (int k = lane; k < np; k += 32) Ls += p.ws_l[base + k] * exp2f(p.ws_m[base + k] - M);
 #pragma unroll
   for (int off = 16; off >= 1; off >>= 1) Ls += __shfl_xor_sync(FULL, Ls, off);
@@ -645,19 +715,20 @@ __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReducePar
   for (int k = 0; k < DPL; ++k) acc[k] = 0.f;
   for (int k = 0; k < np; ++k) {
     const float f = exp2f(p.ws_m[base + k] - M);
+    if (RULE && p.ws_m[base + k] == -INFINITY) continue;
     const float* src = p.ws_o + (base + k) * DH + lane * DPL;
 #pragma unroll
     for (int e = 0; e < DPL; ++e) acc[e] = fmaf(f, src[e], acc[e]);
   }
   T* dst = static_cast<T*>(p.out) + row * DH + lane * DPL;
-  const float inv = 1.f / Ls;
+  const float inv = RULE && Ls == 0.f ? 0.f : 1.f / Ls;
 #pragma unroll
   for (int e = 0; e < DPL; ++e) dst[e] = Elem<T>::from_float(acc[e] * inv);
 }
 
-template <typename T, int G>
+template <typename T, int G, bool RULE>
 cudaError_t launch_mq_t(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
-  auto kern = decode_mq_kernel<T, G>;
+  auto kern = decode_mq_kernel<T, G, RULE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
@@ -689,6 +760,8 @@ cudaError_t launch_mq_t(const MqArgs& a, unsigned int* status, cudaStream_t stre
   p.partition_size = a.partition_size;
   p.num_partitions = a.num_partitions;
   p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.rule = make_rule(a.rule, a.scale);
+  if (RULE) p.scale_log2 = p.rule.scale;
   const int qblocks = (a.max_query_len + MR / G - 1) / (MR / G);
   const int pairs = (qblocks + NT - 1) / NT;
   dim3 grid(a.num_seqs, a.Hkv, pairs * a.num_partitions);
@@ -711,18 +784,22 @@ cudaError_t launch_mq_reduce_t(const MqArgs& a, cudaStream_t stream) {
   p.direct_qblock = a.direct_qblock > 0 ? a.direct_qblock : NT * (MR / (a.Hq / a.Hkv));
   p.partition_size = a.partition_size;
   p.num_partitions = a.num_partitions;
+  p.block_size = a.block_size;
+  p.rule = make_rule(a.rule, a.scale);
   const int64_t warps = static_cast<int64_t>(a.total_q) * a.Hq;
   const unsigned grid = static_cast<unsigned>((warps + 3) / 4);
+  if (a.has_rule)
+    return launch_overlapped(decode_mq_reduce_kernel<T, true>, dim3(grid), dim3(128), 0, stream, p);
   return launch_overlapped(decode_mq_reduce_kernel<T>, dim3(grid), dim3(128), 0, stream, p);
 }
 
-template <typename T>
+template <typename T, bool RULE>
 cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
   switch (a.Hq / a.Hkv) {
-    case 1: return launch_mq_t<T, 1>(a, status, stream);
-    case 2: return launch_mq_t<T, 2>(a, status, stream);
-    case 4: return launch_mq_t<T, 4>(a, status, stream);
-    case 8: return launch_mq_t<T, 8>(a, status, stream);
+    case 1: return launch_mq_t<T, 1, RULE>(a, status, stream);
+    case 2: return launch_mq_t<T, 2, RULE>(a, status, stream);
+    case 4: return launch_mq_t<T, 4, RULE>(a, status, stream);
+    case 8: return launch_mq_t<T, 8, RULE>(a, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -731,8 +808,11 @@ cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stre
 
 int launch_decode_mq(const MqArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16>(a, status, st)
-                            : launch_mq_g<__half>(a, status, st);
+  if (a.has_rule)
+    return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16, true>(a, status, st)
+                              : launch_mq_g<__half, true>(a, status, st);
+  return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16, false>(a, status, st)
+                            : launch_mq_g<__half, false>(a, status, st);
 }
 
 int launch_decode_mq_reduce(const MqArgs& a, void* stream) {

@@ -45,6 +45,7 @@
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "pa_rule.cuh"
 #include "tc_common.cuh"
 
 namespace pa {
@@ -199,13 +200,18 @@ struct TcParams {
   // partitions each, partials from slot_base).
   int span_x;
   int span_ppc;
+  RuleParams rule;   // RULE instances (pa_decode_scored, pa_decode_multi_scored)
 };
 
 // NQ > 1 serves several query tokens per sequence (speculative verification):
 // column c of S / O is query token c / G (one of the sequence's last Qb <= NQ
 // context tokens) with head c % G, and a key counts for it only up to that
 // token's own position.  NQ = 1 is the decode step and compiles as before.
-template <typename T, int G, int NQ = 1, int NP = 16, int CTAS = 2>
+// RULE: capped, distance-biased, windowed scores (pa_rule.cuh).  The sequence is
+// taken from the block of the first key that any of its query tokens sees (the
+// shift of a grouped decode, found here), up to the last one; a column's own
+// limits are then relative to that block.
+template <typename T, int G, int NQ = 1, int NP = 16, int CTAS = 2, bool RULE = false>
 __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
     decode_partition_tc_kernel(const TcParams p, const __grid_constant__ CUtensorMap tmap_k,
                                const __grid_constant__ CUtensorMap tmap_v) {
@@ -319,6 +325,27 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
     }
     L -= shift;
   }
+  int first = 0;            // RULE: tokens of the first block that no query token sees
+  int L_all = L;            // RULE: the sequence's length before it is cut to what is seen
+  if constexpr (RULE) {
+    // every warp finds the same span; Qall = 1 for the decode
+    const int64_t row0 = multi ? q0 - qoff : b;
+    int lo, hi;
+    rule_span(p.rule, b, row0, L - Qall, L, 0, L > 0 ? Qall : 0, lo, hi);
+    if (lo > hi) {
+      // nothing is seen by any query token of the sequence: zero rows
+      if (part == 0) {
+        for (int i = threadIdx.x; i < Qb * G * DH; i += KTHREADS) {
+          const int64_t hq = (static_cast<int64_t>(q0) + i / (G * DH)) * p.Hq + g * G + i / DH % G;
+          static_cast<T*>(p.out)[hq * DH + i % DH] = Elem<T>::from_float(0.f);
+        }
+      }
+      return;
+    }
+    shift = lo / bs * bs;
+    first = lo - shift;
+    L = hi + 1 - shift;
+  }
   const int slot0 = grouped ? 0 : p.slot_base;        // this CTA's first workspace slot
   const int64_t grid_cap = static_cast<int64_t>(p.num_partitions - slot0) * P;
   if (L > grid_cap) {
@@ -327,7 +354,7 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
   }
   const int start = part * P;
   if (L == 0) {
-    if (!grouped && !multi && part == 0 && shift == 0) {
+    if (!RULE && !grouped && !multi && part == 0 && shift == 0) {
       T* o = static_cast<T*>(p.out) + (static_cast<int64_t>(b) * p.Hq + g * G) * DH;
       for (int i = threadIdx.x; i < G * DH; i += KTHREADS) o[i] = Elem<T>::from_float(0.f);
     }
@@ -339,7 +366,7 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
   const int n_tiles = (end - start + TOK - 1) / TOK;
   // the output directly, or partials for the reduce (always for a group's span
   // and for a sequence whose first tokens its group served)
-  const bool single = (L <= P) && !grouped && shift == 0;
+  const bool single = (L <= P) && !grouped && (shift == 0 || RULE);
   const int n_slots = min(ppc, (L + P - 1) / P - part);   // partials this CTA writes
 
   // ---- set-up: the producer starts streaming right after the barrier, while
@@ -509,6 +536,30 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
       m_run[h] = M_NONE;
       l_part[h] = 0.f;
     }
+    // RULE: this thread's query tokens c0 / G + u: the key positions that each
+    // sees and its own, counted from the span's first block, and the slope
+    // of each of the G heads in base 2
+    constexpr int NU = RULE ? (NCH + G - 1) / G : 1;
+    int lo_u[NU], hi_u[NU], pos_u[NU];
+    float slope[RULE ? G : 1];
+    if constexpr (RULE) {
+#pragma unroll
+      for (int u = 0; u < NU; ++u) {
+        const int qi = c0 / G + u;
+        lo_u[u] = 0;
+        hi_u[u] = -1;
+        pos_u[u] = L_all - Qall + qoff + qi - shift;
+        if (qi < Qb) {
+          rule_limits(p.rule, b, static_cast<int64_t>(q0) + qi, L_all - Qall + qoff + qi, L_all,
+                      lo_u[u], hi_u[u]);
+          lo_u[u] -= shift;
+          hi_u[u] -= shift;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < G; ++h)
+        slope[h] = p.rule.slopes != nullptr ? __ldcg(p.rule.slopes + g * G + h) * kLog2e : 0.f;
+    }
     // A failed (timed-out) wait makes `ok` false for the whole warp; later waits
     // are then skipped, but every named barrier is still joined so the
     // softmax warps never wait on each other forever.
@@ -549,7 +600,8 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
           const int64_t hq = (static_cast<int64_t>(q0) + hg / G) * p.Hq + g * G + hg % G;
           if (NQ > 1 && hg / G >= Qb) continue;
           if (single) {
-            static_cast<T*>(p.out)[hq * DH + r] = Elem<T>::from_float(o[h] / Ls);
+            const bool none = RULE && Ls == 0.f;   // this query token sees nothing
+            static_cast<T*>(p.out)[hq * DH + r] = Elem<T>::from_float(none ? 0.f : o[h] / Ls);
           } else {
             const int64_t slot = hq * p.num_partitions + slot0 + part;
             p.ws_o[slot * DH + r] = o[h];
@@ -587,6 +639,15 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
 #pragma unroll
       for (int h = 0; h < NCH; ++h) {
         bool ok_h = valid;
+        if constexpr (RULE) {
+          const int u = h / G, j = start + i * TOK + r;
+          ok_h = j >= lo_u[u] && j <= hi_u[u];
+          const float x = rule_score(p.rule, sv[h] * p.scale_log2, slope[h % G],
+                                     fabsf(static_cast<float>(pos_u[u] - j)));
+          s[h] = ok_h ? x : -INFINITY;
+          need |= s[h] > m_run[h] + RESCALE_THRESHOLD;
+          continue;
+        }
         if constexpr (NQ > 1) {  // causal: up to query token hg / G's own position
           const int hg = c0 + h;
           ok_h = ok_h && hg / G < Qb && start + i * TOK + r <= L - Qall + qoff + hg / G;
@@ -648,7 +709,8 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
         }
         *reinterpret_cast<uint4*>(pb + (c0 / 8 + c) * P_CHUNK) = make_uint4(w[0], w[1], w[2], w[3]);
       }
-      if (n_valid < TOK && hf == 0) {
+      const int n_first = RULE ? first - (start + i * TOK) : 0;   // > 0 in the first tile only
+      if ((n_valid < TOK || (RULE && n_first > 0)) && hf == 0) {
         // the last tile: zero the V rows of tokens past the end, so that
         // whatever they hold (unused slots, stale data) adds 0 * 0 to O (one
         // half's warps do it; the MMA waits for every softmax warp)
@@ -660,7 +722,7 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
         // that read it, or the zeroing could come before tile i's V lands and
         // bring back whatever the cache holds past the context.
         if (SLOTS == 2 && i > 0) wait(&p_free[(i - 1) % PBUF], ((i - 1) / PBUF) & 1);
-        if (wait(&ring_full[s_], (u / SLOTS) & 1) && !valid) {
+        if (wait(&ring_full[s_], (u / SLOTS) & 1) && (!valid || (RULE && r < n_first))) {
           uint8_t* row = ring + s_ * SLOT_BYTES + (r >> 3) * GROUP_BYTES + (r & 7) * 128;
 #pragma unroll
           for (int c = 0; c < 8; ++c) {
@@ -690,10 +752,10 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
 
 // ---- host side ----
 
-template <typename T, int G>
+template <typename T, int G, bool RULE = false>
 cudaError_t launch_tc_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
   const int ppc = tc_parts_per_cta(a);
-  auto kern = decode_partition_tc_kernel<T, G>;
+  auto kern = decode_partition_tc_kernel<T, G, 1, 16, 2, RULE>;
   constexpr int SMEM_BYTES = Lay<16>::SMEM_BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess)   // all of the SM's 228 KB as shared memory: two CTAs of up to 113 KB
@@ -737,6 +799,8 @@ cudaError_t launch_tc_t(const DecodeArgs& a, unsigned int* status, cudaStream_t 
   p.slot_base = a.slot_base;
   p.span_x = 0;
   p.span_ppc = 1;
+  p.rule = make_rule(a.rule, a.scale);
+  if (RULE) p.scale_log2 = p.rule.scale;
   const int np = a.num_partitions - a.slot_base;
   dim3 grid(a.num_seqs, a.Hkv, (np + p.parts_per_cta - 1) / p.parts_per_cta);
   return launch_overlapped(kern, grid, dim3(tc_threads<16>()), SMEM_BYTES, stream, p, mk, mv);
@@ -870,12 +934,12 @@ bool tmap_available() { return encode_fn() != nullptr; }
 
 namespace {
 
-template <typename T, int G, int NQ, int NP = 16>
+template <typename T, int G, int NQ, int NP, bool RULE>
 cudaError_t launch_tcq_t(const MqArgs& m, unsigned int* status, cudaStream_t stream) {
   const int q_groups = (m.max_query_len + NQ - 1) / NQ;
   const int ppc = tc_parts_per_cta(static_cast<int64_t>(m.num_seqs) * q_groups * m.Hkv,
                                    m.partition_size, m.num_partitions, 0);
-  auto kern = decode_partition_tc_kernel<T, G, NQ, NP>;
+  auto kern = decode_partition_tc_kernel<T, G, NQ, NP, 2, RULE>;
   constexpr int SMEM_BYTES = Lay<NP>::SMEM_BYTES;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e == cudaSuccess)   // all of the SM's 228 KB as shared memory: two CTAs of up to 113 KB
@@ -916,6 +980,8 @@ cudaError_t launch_tcq_t(const MqArgs& m, unsigned int* status, cudaStream_t str
   p.slot_base = 0;
   p.span_x = 0;
   p.span_ppc = 1;
+  p.rule = make_rule(m.rule, m.scale);
+  if (RULE) p.scale_log2 = p.rule.scale;
   dim3 grid(m.num_seqs * p.q_groups, m.Hkv, (m.num_partitions + ppc - 1) / ppc);
   return launch_overlapped(kern, grid, dim3(tc_threads<NP>()), SMEM_BYTES, stream, p, mk, mv);
 }
@@ -923,17 +989,17 @@ cudaError_t launch_tcq_t(const MqArgs& m, unsigned int* status, cudaStream_t str
 // Query tokens per CTA (tc_query_tokens_per_cta): up to 16 columns on the
 // N = 16 kernel, else 32 columns on the N = 32 kernel, so 4 tokens at G = 8
 // (or 8 at G = 4) share one read of the sequence's K/V.
-template <typename T>
+template <typename T, bool RULE>
 cudaError_t launch_tcq_g(const MqArgs& m, unsigned int* status, cudaStream_t stream) {
   const int G = m.Hq / m.Hkv;
   const int nq = tc_query_tokens_per_cta(G, m.max_query_len);
   if (G == 8) {
-    return nq == 2 ? launch_tcq_t<T, 8, 2>(m, status, stream)
-                   : launch_tcq_t<T, 8, 4, 32>(m, status, stream);
+    return nq == 2 ? launch_tcq_t<T, 8, 2, 16, RULE>(m, status, stream)
+                   : launch_tcq_t<T, 8, 4, 32, RULE>(m, status, stream);
   }
-  return nq == 2 ? launch_tcq_t<T, 4, 2>(m, status, stream)
-       : nq == 4 ? launch_tcq_t<T, 4, 4>(m, status, stream)
-                 : launch_tcq_t<T, 4, 8, 32>(m, status, stream);
+  return nq == 2 ? launch_tcq_t<T, 4, 2, 16, RULE>(m, status, stream)
+       : nq == 4 ? launch_tcq_t<T, 4, 4, 16, RULE>(m, status, stream)
+                 : launch_tcq_t<T, 4, 8, 32, RULE>(m, status, stream);
 }
 
 }  // namespace
@@ -950,8 +1016,11 @@ bool decode_mq_tc_supported(const MqArgs& m) {
 
 int launch_decode_mq_tc(const MqArgs& m, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return m.dtype == PA_BF16 ? launch_tcq_g<__nv_bfloat16>(m, status, st)
-                            : launch_tcq_g<__half>(m, status, st);
+  if (m.has_rule)
+    return m.dtype == PA_BF16 ? launch_tcq_g<__nv_bfloat16, true>(m, status, st)
+                              : launch_tcq_g<__half, true>(m, status, st);
+  return m.dtype == PA_BF16 ? launch_tcq_g<__nv_bfloat16, false>(m, status, st)
+                            : launch_tcq_g<__half, false>(m, status, st);
 }
 
 bool decode_tc_supported(const DecodeArgs& a) {
@@ -1010,6 +1079,13 @@ int launch_decode_group_tc(const DecodeArgs& a, unsigned int* status, void* stre
 int launch_decode_partitions_tc(const DecodeArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int G = a.Hq / a.Hkv;
+  if (a.has_rule) {
+    if (a.dtype == PA_BF16)
+      return G == 8 ? launch_tc_t<__nv_bfloat16, 8, true>(a, status, st)
+                    : launch_tc_t<__nv_bfloat16, 4, true>(a, status, st);
+    return G == 8 ? launch_tc_t<__half, 8, true>(a, status, st)
+                  : launch_tc_t<__half, 4, true>(a, status, st);
+  }
   if (a.dtype == PA_BF16) {
     return G == 8 ? launch_tc_t<__nv_bfloat16, 8>(a, status, st)
                   : launch_tc_t<__nv_bfloat16, 4>(a, status, st);

@@ -164,6 +164,9 @@ struct Tc8Params {
   int slot_base;
   int total_q;       // num_seqs
   int q_groups;      // CTAs per group along x (members / NQ, rounded up)
+  // BS: one scale per (physical block, kv head), [NB][Hkv]
+  const float* k_scales;
+  const float* v_scales;
 };
 
 // Four E4M3 codes (one 32-bit word, code i in byte i) -> two f16x2 words
@@ -189,7 +192,13 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 
 // NQ = 1 is the decode (one sequence per CTA, its G heads the columns); NQ > 1
 // serves a group's shared span for NQ members at once (G * NQ <= 16 columns).
-template <typename T, int G, typename Y, int NQ = 1>
+// BS (pa_decode_fp8_block): a scale per (physical block, kv head) instead of the
+// caches' two.  A softmax thread owns one token row, so both scales are one
+// number to it: the key scale joins the score's factor, the value scale its
+// exponent (P = 2^(s + log2 vs - m) weights the raw codes, and the running max
+// guards the products p vs), and the partial sum adds P / vs.  The thread reads
+// its block's scales a tile ahead and the block's id two.
+template <typename T, int G, typename Y, int NQ = 1, bool BS = false>
 __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     decode_partition_tc8_kernel(const Tc8Params p, const __grid_constant__ CUtensorMap tmap_k,
                                 const __grid_constant__ CUtensorMap tmap_v) {
@@ -505,6 +514,22 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       l_part[h] = 0.f;
       sc[h] = p.scale_log2 * qs[h];
     }
+    int pb_next = -1;
+    float ks_next = 1.f, vs_next = 1.f;
+    auto block_of = [&](int i) -> int {
+      const int j = start + i * TOK + r;
+      return i < n_tiles && j < end ? __ldcg(trow + j / bs) : -1;
+    };
+    auto scales_of = [&](int pb) {
+      const bool in = pb >= 0 && pb < p.num_blocks;
+      const int64_t at = static_cast<int64_t>(in ? pb : 0) * p.Hkv + g;
+      ks_next = in ? __ldcg(p.k_scales + at) : 1.f;
+      vs_next = in ? __ldcg(p.v_scales + at) : 1.f;
+    };
+    if constexpr (BS) {
+      scales_of(block_of(0));
+      pb_next = block_of(1);
+    }
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok) ok = mbar_wait(bar, parity, p.status);
@@ -563,6 +588,15 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     for (int i = 0; i < n_tiles; ++i) {
       const int n_valid = min(TOK, end - (start + i * TOK));
       const bool valid = r < n_valid;
+      float ks = 1.f, lvs = 0.f, rvs = 1.f;
+      if constexpr (BS) {
+        const float vs = fminf(fmaxf(vs_next, kScaleMin), kScaleMax);
+        ks = fminf(fmaxf(ks_next, kScaleMin), kScaleMax);
+        lvs = __log2f(vs);
+        rvs = __frcp_rn(vs);
+        scales_of(pb_next);
+        pb_next = block_of(i + 2);
+      }
       float sv[16];
       if (wait(&s_full[i & 1], (i >> 1) & 1)) {
         tc_fence_after();
@@ -578,7 +612,7 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       bool need = false;
 #pragma unroll
       for (int h = 0; h < NC; ++h) {
-        s[h] = valid && h / G < Qb ? sv[h] * sc[h] : -INFINITY;
+        s[h] = valid && h / G < Qb ? (BS ? fmaf(sv[h] * sc[h], ks, lvs) : sv[h] * sc[h]) : -INFINITY;
         need |= s[h] > m_run[h] + RESCALE_THRESHOLD;
       }
       if (bar_or(1, 128, need)) {
@@ -614,7 +648,7 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
 #pragma unroll
       for (int h = 0; h < NC; ++h) {
         pr[h] = s[h] != -INFINITY ? ex2_fast(s[h] - m_run[h]) : 0.f;
-        l_part[h] += pr[h];
+        l_part[h] = BS ? fmaf(pr[h], rvs, l_part[h]) : l_part[h] + pr[h];
       }
       if (i >= PBUF) wait(&p_free[i % PBUF], ((i / PBUF) - 1) & 1);
       // P * 2^6 = P1 + P2, two E4M3 codes per head (heads h, h+1 in one pair);
@@ -700,7 +734,7 @@ int tc8_parts_per_cta(int64_t rows, int partition_size, int n_parts, int64_t oth
 // from a.slot_base).  NQ = 16 / G: the groups' shared spans, one CTA per
 // (group, run of NQ members, kv head, run of span partitions), partials into
 // slots [0, a.slot_base) of every member's row.
-template <typename T, int G, int NQ>
+template <typename T, int G, int NQ, bool BS = false>
 cudaError_t launch_tc8_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
   using Y = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, LayBF16, LayF16>::type;
   constexpr int SMEM_BYTES = Y::SMEM_BYTES;
@@ -711,7 +745,7 @@ cudaError_t launch_tc8_t(const DecodeArgs& a, unsigned int* status, cudaStream_t
   int64_t other = 0;      // the rest's CTAs next to the spans: one per (sequence, head, partition)
   if (grouped) other = static_cast<int64_t>(a.num_seqs) * a.Hkv * (a.num_partitions - a.slot_base);
   const int ppc = tc8_parts_per_cta(xs * a.Hkv, a.partition_size, n_parts, other);
-  auto kern = decode_partition_tc8_kernel<T, G, Y, NQ>;
+  auto kern = decode_partition_tc8_kernel<T, G, Y, NQ, BS>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   // each cache [NB][Hkv][bs][128] as rows of 128 codes; a box is the bs rows of
@@ -749,6 +783,8 @@ cudaError_t launch_tc8_t(const DecodeArgs& a, unsigned int* status, cudaStream_t
   p.slot_base = grouped ? 0 : a.slot_base;
   p.total_q = a.num_seqs;
   p.q_groups = q_groups;
+  p.k_scales = a.k_scales;
+  p.v_scales = a.v_scales;
   if (xs <= 0 || xs > 0x7fffffff) return cudaErrorInvalidValue;
   dim3 grid(static_cast<unsigned>(xs), a.Hkv, (n_parts + ppc - 1) / ppc);
   return launch_overlapped(kern, grid, dim3(THREADS), SMEM_BYTES, stream, p, mk, mv);
@@ -767,6 +803,13 @@ bool decode_tc8_supported(const DecodeArgs& a) {
 int launch_decode_partitions_tc8(const DecodeArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int G = a.Hq / a.Hkv;
+  if (a.k_scales != nullptr) {
+    if (a.dtype == PA_BF16)
+      return G == 8 ? launch_tc8_t<__nv_bfloat16, 8, 1, true>(a, status, st)
+                    : launch_tc8_t<__nv_bfloat16, 4, 1, true>(a, status, st);
+    return G == 8 ? launch_tc8_t<__half, 8, 1, true>(a, status, st)
+                  : launch_tc8_t<__half, 4, 1, true>(a, status, st);
+  }
   if (a.dtype == PA_BF16) {
     return G == 8 ? launch_tc8_t<__nv_bfloat16, 8, 1>(a, status, st)
                   : launch_tc8_t<__nv_bfloat16, 4, 1>(a, status, st);

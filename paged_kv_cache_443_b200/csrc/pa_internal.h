@@ -67,7 +67,30 @@ struct DecodeArgs {
   // the group launch: members group_start[i] .. group_start[i+1]-1 (device)
   const int32_t* group_start = nullptr;
   int num_groups = 0, max_group_size = 0;
+  // An E4M3 cache with a scale per (block, kv head) (pa_decode_fp8_block):
+  // [NB][Hkv] (device); k_scale = v_scale = 1 then
+  const float* k_scales = nullptr;
+  const float* v_scales = nullptr;
+  // pa_decode_scored; num_partitions then counts from a sequence's first
+  // visible block (rule_span_bound)
+  bool has_rule = false;
+  pa_score_rule rule = {};
 };
+
+// The scales that the kernels take a block of codes to have: a stored value
+// outside is read as the nearer bound (their 1 / scale stays finite, and the
+// weights of two blocks stay within the range of an fp32).
+constexpr float kScaleMin = 9.094947017729282e-13f;  // 2^-40
+constexpr float kScaleMax = 1.2089258196146292e+24f; // 2^80
+
+// Most tokens from the first visible block to the last visible key of a run of
+// run_len query tokens under a rule, for contexts up to max_context_len.
+inline int rule_span_bound(const pa_score_rule& r, int max_context_len, int run_len,
+                           int block_size) {
+  if (r.window <= 0 || r.prefix_lens != nullptr) return max_context_len;
+  const int64_t n = static_cast<int64_t>(r.window) + run_len + block_size;
+  return n < max_context_len ? static_cast<int>(n) : max_context_len;
+}
 
 // Kernel launchers (kernels.cu).  They return cudaError_t as int.
 int launch_decode_partitions(const DecodeArgs& a, unsigned int* status, void* stream);
@@ -124,6 +147,10 @@ struct MqArgs {
   // run's outputs directly, with no partials, when its last query token's last
   // key lies in the first partition.
   int direct_qblock = 0;
+  // pa_decode_multi_scored: partitions then count from the first visible block
+  // of each run of direct_qblock query tokens (set before the launches)
+  bool has_rule = false;
+  pa_score_rule rule = {};
 };
 constexpr int kMqRows = 128;  // (query token, head) rows per query tile of the multi-query kernel
 constexpr int kMqTiles = 2;   // query tiles per CTA of the multi-query kernel
@@ -152,6 +179,21 @@ int launch_reshape_and_cache_fp8(const void* key, const void* value, void* k_cac
                                  void* v_cache, const int64_t* slot_mapping, int num_tokens,
                                  int Hkv, int D, int block_size, int num_blocks, pa_dtype dtype,
                                  float k_scale, float v_scale, unsigned int* status, void* stream);
+// Append into an E4M3 cache with a scale per (block, kv head) (cache_block.cu).
+int launch_append_block(const void* key, const void* value, void* k_cache, void* v_cache,
+                        float* k_scales, float* v_scales, const int64_t* slot_mapping,
+                        int num_tokens, int Hkv, int D, int block_size, int num_blocks,
+                        pa_dtype dtype, unsigned int* status, void* stream);
+// Block copies of such a cache, codes and scales ([0]: keys, [1]: values).
+struct CopyScaled {
+  void* dst[2];
+  const void* src[2];
+  float* dst_scales[2];
+  const float* src_scales[2];
+  const int64_t* pairs;
+  int num_pairs, src_blocks, dst_blocks, Hkv, D, block_size;
+};
+int launch_copy_block_scaled(const CopyScaled& c, unsigned int* status, void* stream);
 int launch_copy_blocks(void* dst_k, void* dst_v, const void* src_k, const void* src_v,
                        const int64_t* pairs, int num_pairs, int Hkv, int D, int block_size,
                        int src_blocks, int dst_blocks, int esize, unsigned int* status,
