@@ -161,13 +161,27 @@ def _check(st: int) -> None:
         raise (OutOfBlocks if st == PA_ERR_OOM else PagedKVError)(st, msg)
 
 
+_torch = None
+_codes = {}
+
+
+def _t():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _codes.update({torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
+                       torch.float8_e4m3fn: PA_FP8_E4M3})
+        _torch = torch
+    return _torch
+
+
 def _dtype_code(t) -> int:
-    import torch
-    codes = {torch.float32: PA_F32, torch.float16: PA_F16, torch.bfloat16: PA_BF16,
-             torch.float8_e4m3fn: PA_FP8_E4M3}
-    if t.dtype not in codes:
+    _t()
+    code = _codes.get(t.dtype)
+    if code is None:
         raise PagedKVError(PA_ERR_INVALID, f"unsupported dtype {t.dtype}")
-    return codes[t.dtype]
+    return code
 
 
 def _ptr(t) -> Optional[int]:
@@ -176,8 +190,9 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        torch = _t()
+        # the raw handle: a Stream object of it takes several microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -190,9 +205,9 @@ def _contig(*ts):
 def _current_device(*ts):
     """Refuses device tensors that are not on the current CUDA device (kernels run
     there, on its current stream unless one is given)."""
-    import torch
+    dev = _t().cuda.current_device() if ts[0].is_cuda else -2
     for t in ts:
-        if t is not None and (t.device.type != "cuda" or t.device.index != torch.cuda.current_device()):
+        if t is not None and t.get_device() != dev:
             raise PagedKVError(PA_ERR_INVALID,
                                f"tensors must be on the current CUDA device (got {t.device})")
 
@@ -262,23 +277,26 @@ def pa_decode_workspace_bytes(num_seqs: int, num_heads: int, head_size: int,
 def _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                  max_context_len, workspace, stream, kv_dtype=None):
     _contig(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
-    B, Hq, D = q.shape
-    NB, Hkv, bs, D2 = k_cache.shape
-    if D2 != D or tuple(out.shape) != (B, Hq, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
+    B, Hq, D = shape = q.shape
+    NB, Hkv, bs, D2 = pool = k_cache.shape
+    if D2 != D or out.shape != shape or v_cache.shape != pool:
         raise PagedKVError(PA_ERR_INVALID, "shape mismatch among q, out and the caches")
-    for t, want in ((out, q.dtype), (k_cache, kv_dtype or q.dtype), (v_cache, kv_dtype or q.dtype)):
-        if t.dtype != want:
-            raise PagedKVError(PA_ERR_INVALID, f"dtype mismatch: {t.dtype} where {want} is expected")
-    import torch
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    dtype = q.dtype
+    kv_dtype = kv_dtype or dtype
+    if out.dtype != dtype or k_cache.dtype != kv_dtype or v_cache.dtype != kv_dtype:
+        for t, want in ((out, dtype), (k_cache, kv_dtype), (v_cache, kv_dtype)):
+            if t.dtype != want:
+                raise PagedKVError(PA_ERR_INVALID,
+                                   f"dtype mismatch: {t.dtype} where {want} is expected")
+    int32 = _t().int32
+    if block_tables.dtype != int32 or context_lens.dtype != int32:
         raise PagedKVError(PA_ERR_INVALID, "block_tables and context_lens must be int32")
     if max_context_len is None:
         raise PagedKVError(PA_ERR_INVALID, "max_context_len is required (an upper bound)")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    return (_ptr(out), _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
-            block_tables.shape[1], _ptr(context_lens), B, Hq, Hkv, D, bs, NB, float(scale),
-            _dtype_code(q), int(partition_size), int(max_context_len), _ptr(workspace), ws_bytes,
-            _stream(stream))
+    return (out.data_ptr(), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+            block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(), B, Hq, Hkv,
+            D, bs, NB, float(scale), _dtype_code(q), int(partition_size), int(max_context_len),
+            _ptr(workspace), 0 if workspace is None else workspace.nbytes, _stream(stream))
 
 
 def pa_decode(out, q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len,
@@ -308,7 +326,7 @@ class Groups:
 def pa_build_groups(block_tables, context_lens, block_size: int) -> Groups:
     """Groups of consecutive sequences sharing leading physical blocks, from
     host (CPU) int32 block tables [B, max_blocks] and context lengths [B]."""
-    import torch
+    torch = _t()
     t = block_tables.to("cpu", torch.int32).contiguous()
     l = context_lens.to("cpu", torch.int32).contiguous()
     B, mb = t.shape
@@ -346,7 +364,7 @@ def pa_decode_grouped_fp8(out, q, k_cache, v_cache, block_tables, context_lens, 
                           workspace=None, stream=None) -> None:
     """pa_decode_fp8's result over E4M3 caches, with each group's shared span
     read once for all its members."""
-    import torch
+    torch = _t()
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
     _contig(groups.group_start, groups.shared_lens)
@@ -377,7 +395,7 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, m
                   k_scale, v_scale, partition_size=0, workspace=None, stream=None) -> None:
     """pa_decode over E4M3 caches (torch.float8_e4m3fn): keys stand for
     code * k_scale, values for code * v_scale; q and out f32 / f16 / bf16."""
-    import torch
+    torch = _t()
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
     _check(lib().pa_decode_fp8(*a[:15], float(k_scale), float(v_scale), *a[15:]))
@@ -386,7 +404,7 @@ def pa_decode_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale, m
 def pa_decode_partitions_fp8(out, q, k_cache, v_cache, block_tables, context_lens, scale,
                              max_context_len, k_scale, v_scale, partition_size=0, workspace=None,
                              stream=None) -> None:
-    import torch
+    torch = _t()
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
     _check(lib().pa_decode_partitions_fp8(*a[:15], float(k_scale), float(v_scale), *a[15:]))
@@ -397,7 +415,7 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale
     """Store key/value (f32 / f16 / bf16) as E4M3 codes of x / scale in the
     float8_e4m3fn caches at their slots."""
     _contig(key, value, k_cache, v_cache, slot_mapping)
-    import torch
+    torch = _t()
     N, Hkv, D = key.shape
     NB, Hkv2, bs, D2 = k_cache.shape
     if (Hkv2, D2) != (Hkv, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
@@ -413,9 +431,9 @@ def pa_reshape_and_cache_fp8(key, value, k_cache, v_cache, slot_mapping, k_scale
 
 def _scales(cache, *scales):
     """Checks the [num_blocks, Hkv] float32 scales of an E4M3 cache."""
-    import torch
+    f32, shape = _t().float32, cache.shape[:2]
     for t in scales:
-        if (t.dtype != torch.float32 or tuple(t.shape) != tuple(cache.shape[:2])):
+        if t.dtype != f32 or t.shape != shape:
             raise PagedKVError(PA_ERR_INVALID, "scales must be float32 [num_blocks, Hkv]")
     _contig(*scales)
 
@@ -426,13 +444,13 @@ def pa_decode_fp8_block(out, q, k_cache, v_cache, k_scales, v_scales, block_tabl
     """pa_decode over E4M3 caches with a scale per (block, kv head): codes of
     block i and kv head h stand for code * k_scales[i, h] (v_scales for values);
     q and out f32 / f16 / bf16."""
-    import torch
+    torch = _t()
     _current_device(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
                     workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
     _scales(k_cache, k_scales, v_scales)
-    if context_lens.numel() != q.shape[0] or block_tables.shape[0] != q.shape[0]:
+    if context_lens.numel() != a[7] or block_tables.shape[0] != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
     _check(lib().pa_decode_fp8_block(*a[:4], _ptr(k_scales), _ptr(v_scales), *a[4:]))
 
@@ -445,7 +463,7 @@ def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_sca
     starts anew); the block's older codes follow when it grows.  The tokens of a
     block stand next to each other in slot_mapping."""
     _contig(key, value, k_cache, v_cache, slot_mapping)
-    import torch
+    torch = _t()
     N, Hkv, D = key.shape
     NB, Hkv2, bs, D2 = k_cache.shape
     if (Hkv2, D2) != (Hkv, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
@@ -462,7 +480,7 @@ def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_sca
 
 
 def _scaled_pool(k_cache, v_cache, k_scales, v_scales):
-    import torch
+    torch = _t()
     _contig(k_cache, v_cache)
     if v_cache.shape != k_cache.shape:
         raise PagedKVError(PA_ERR_INVALID, "cache shape mismatch")
@@ -478,7 +496,7 @@ def _scaled_pool(k_cache, v_cache, k_scales, v_scales):
 
 
 def _pairs(block_pairs):
-    import torch
+    torch = _t()
     _contig(block_pairs)
     if block_pairs.dtype != torch.int64 or (block_pairs.numel() and block_pairs.shape[-1] != 2):
         raise PagedKVError(PA_ERR_INVALID, "block_pairs must be int64 [P, 2]")
@@ -523,7 +541,7 @@ def pa_decode_multi_workspace_bytes(total_q: int, num_heads: int, head_size: int
 def _multi_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
                 max_context_len, max_query_len, partition_size, workspace, stream):
     _contig(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace)
-    import torch
+    torch = _t()
     T, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_cache.shape
     if D2 != D or tuple(out.shape) != (T, Hq, D) or tuple(v_cache.shape) != tuple(k_cache.shape):
@@ -570,20 +588,21 @@ class ScoreRule:
         self.alibi_slopes, self.key_starts, self.prefix_lens = alibi_slopes, key_starts, prefix_lens
 
     def _struct(self, q, num_seqs: int) -> _ScoreRule:
-        import torch
-        rows, heads = q.shape[0], q.shape[1]
-        for name, n, dtype in (("alibi_slopes", heads, torch.float32),
-                               ("key_starts", rows, torch.int32),
-                               ("prefix_lens", num_seqs, torch.int32)):
-            t = getattr(self, name)
-            if t is None:
-                continue
-            if t.dtype != dtype or tuple(t.shape) != (n,) or t.device != q.device:
-                raise PagedKVError(PA_ERR_INVALID,
-                                   f"{name} must be {dtype} [{n}] on the queries' device")
-            _contig(t)
-        return _ScoreRule(self.softcap, self.window, _ptr(self.alibi_slopes),
-                          _ptr(self.key_starts), _ptr(self.prefix_lens))
+        torch = _t()
+        slopes, starts, prefix = self.alibi_slopes, self.key_starts, self.prefix_lens
+        if slopes is not None:
+            self._check("alibi_slopes", slopes, q.shape[1], torch.float32, q)
+        if starts is not None:
+            self._check("key_starts", starts, q.shape[0], torch.int32, q)
+        if prefix is not None:
+            self._check("prefix_lens", prefix, num_seqs, torch.int32, q)
+        return _ScoreRule(self.softcap, self.window, _ptr(slopes), _ptr(starts), _ptr(prefix))
+
+    @staticmethod
+    def _check(name, t, n, dtype, q):
+        if t.dtype != dtype or t.shape != (n,) or t.get_device() != q.get_device():
+            raise PagedKVError(PA_ERR_INVALID, f"{name} must be {dtype} [{n}] on the queries' device")
+        _contig(t)
 
 
 def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale,
@@ -593,9 +612,9 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale
     _current_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream)
-    if context_lens.numel() != q.shape[0] or block_tables.shape[0] != q.shape[0]:
+    if context_lens.numel() != a[7] or block_tables.shape[0] != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
-    r = rule._struct(q, q.shape[0])
+    r = rule._struct(q, a[7])
     _check(lib().pa_decode_scored(*a[:15], ctypes.byref(r), *a[15:]))
 
 
@@ -629,7 +648,7 @@ def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, context_lens, scal
 def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None) -> None:
     """k_cache[s // bs, h, s % bs] = key[t, h] (same for value) for s = slot_mapping[t] >= 0."""
     _contig(key, value, k_cache, v_cache, slot_mapping)
-    import torch
+    torch = _t()
     N, Hkv, D = key.shape
     NB, Hkv2, bs, D2 = k_cache.shape
     if (Hkv2, D2) != (Hkv, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
@@ -646,7 +665,7 @@ def pa_reshape_and_cache(key, value, k_cache, v_cache, slot_mapping, stream=None
 def pa_copy_blocks(k_cache, v_cache, block_pairs, stream=None) -> None:
     """Block block_pairs[p,1] := block block_pairs[p,0] in both caches."""
     _contig(k_cache, v_cache, block_pairs)
-    import torch
+    torch = _t()
     NB, Hkv, bs, D = k_cache.shape
     if block_pairs.dtype != torch.int64 or (block_pairs.numel() and block_pairs.shape[-1] != 2):
         raise PagedKVError(PA_ERR_INVALID, "block_pairs must be int64 [P, 2]")
@@ -663,7 +682,7 @@ def pa_swap_blocks(dst_k_cache, dst_v_cache, src_k_cache, src_v_cache, block_pai
     of the source caches.  A cache pair may be pinned host memory (torch
     pin_memory()); block_pairs is an int64 [P, 2] tensor on the device or pinned."""
     _contig(dst_k_cache, dst_v_cache, src_k_cache, src_v_cache, block_pairs)
-    import torch
+    torch = _t()
     NBd, Hkv, bs, D = dst_k_cache.shape
     NBs = src_k_cache.shape[0]
     if (tuple(src_k_cache.shape[1:]) != (Hkv, bs, D) or src_v_cache.shape != src_k_cache.shape

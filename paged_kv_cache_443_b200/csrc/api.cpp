@@ -593,6 +593,39 @@ pa_status check_rule(const char* fn, const pa_score_rule* r, float scale) {
   return PA_OK;
 }
 
+// The calls under a rule split what a window leaves evenly: with the lengths of
+// the plain calls a window of 4096 leaves a second partition of a block or two,
+// a CTA of fixed costs only (128 sequences, 2.06 GB: 335 us, evenly 330).
+int even_partition(int P, int span) {
+  if (span <= P) return P;
+  const int np = (span + P - 1) / P;
+  return ((span + np - 1) / np + 127) / 128 * 128;
+}
+
+// Partition length for a few query tokens per sequence under a rule (the
+// token-major kernel, two CTAs per SM): a CTA's set-up, first running max and
+// epilogue over up to 32 columns cost it about as much as four 128-token tiles,
+// so splitting pays only while it fills idle SMs.  Takes the even split with
+// the fewest (tiles + 4) * rounds of CTAs; the reduce counts as one more tile
+// (64 sequences of 4 tokens, window 1024: three partitions 114 us, two 97, one
+// 66).  Never shorter than the default where the workspace was sized by it.
+int auto_partition_few(int64_t ctas_per_part, int span) {
+  const int64_t slots = 2ll * num_sms();
+  int best = span < pa::kDefaultPartition ? pa::kDefaultPartition : (span + 127) / 128 * 128;
+  int64_t best_cost = -1;
+  for (int np = 1; np <= (span + pa::kDefaultPartition - 1) / pa::kDefaultPartition; ++np) {
+    const int P = np == 1 ? best : even_partition((span + np - 1) / np, span);
+    if (P < pa::kDefaultPartition) break;
+    const int64_t rounds = (ctas_per_part * np + slots - 1) / slots;
+    const int64_t cost = rounds * ((P + 127) / 128 + 4) + (np > 1 ? 1 : 0);
+    if (best_cost < 0 || cost < best_cost) {
+      best_cost = cost;
+      best = P;
+    }
+  }
+  return best;
+}
+
 // pa_decode_multi, and with a rule pa_decode_multi_scored.
 pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_cache,
                        const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
@@ -611,8 +644,17 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
   }
   if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0 && num_heads % num_kv_heads == 0 &&
       max_query_len > 0 && num_seqs >= 0)
-    partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len, dtype,
-                                          span);
+  {
+    const int G = num_heads / num_kv_heads;
+    if (rule != nullptr && (G == 4 || G == 8) && max_query_len <= 64 / G) {
+      const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
+      partition_size = auto_partition_few(
+          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), span);
+    } else {
+      partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len,
+                                            dtype, span);
+    }
+  }
   if (pa::elem_size(dtype) == 0) return pa::fail(PA_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (dtype != PA_F16 && dtype != PA_BF16)
     return pa::fail(PA_ERR_UNSUPPORTED, "%s: q, out and the caches must be f16 or bf16", fn);
@@ -757,7 +799,8 @@ extern "C" pa_status pa_decode_scored(void* out, const void* q, const void* k_ca
     return pa::fail(PA_ERR_INVALID, "%s: max_context_len %d exceeds max_blocks_per_seq * block_size",
                     fn, max_context_len);
   if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
-    partition_size = auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, span);
+    partition_size = even_partition(
+        auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, span), span);
   pa::DecodeArgs a;
   st = check_decode_full(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                          context_lens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
@@ -826,8 +869,8 @@ extern "C" pa_status pa_reshape_and_cache_fp8_block(const void* key, const void*
     return pa::fail(PA_ERR_INVALID, "%s: key/value/caches must be 16-byte aligned, slots 8", fn);
   st = check_scales(fn, k_scales, v_scales);
   if (st != PA_OK) return st;
-  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t(1) << 31))
-    return pa::fail(PA_ERR_UNSUPPORTED, "%s: num_tokens * num_kv_heads must be below 2^31", fn);
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads >= (int64_t(1) << 30))
+    return pa::fail(PA_ERR_UNSUPPORTED, "%s: num_tokens * num_kv_heads must be below 2^30", fn);
   unsigned int* status = pa::device_status_word();
   if (!status) return PA_ERR_CUDA;
   return launch_status(fn,

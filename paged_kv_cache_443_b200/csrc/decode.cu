@@ -524,7 +524,10 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
 #pragma unroll
         for (int h = 0; h < G; ++h) sl = (h == hh) ? slope[h] : sl;
         const float away = static_cast<float>(L - 1 - (start + t * C::TOK + tl));
-        const float x = rule_score(p.rule, sv[ps], sl, away);
+        // one score per lane and pass: a run-time condition costs nothing here
+        const float x = p.rule.cap_log2 > 0.f
+                            ? rule_score<kRuleCapped>(p.rule, sv[ps], sl, away)
+                            : rule_score<kRuleOpen>(p.rule, sv[ps], sl, away);
         sv[ps] = idx < C::NSM && tl >= n_first && tl < n_valid ? x : -INFINITY;
       }
       float x = sv[ps];

@@ -206,9 +206,9 @@ struct MqParams {
 // RULE: capped, distance-biased, windowed scores (pa_rule.cuh).  The CTA's keys
 // run from the block of the first key that any of its query tokens sees
 // (positions below are counted from there) to the last one; the first pass
-// over a tile's scores applies the rule and leaves the finished scores in TMEM
-// for the second.
-template <typename T, int G, bool RULE = false>
+// over a tile's scores applies the rule to find the maximum, the second once
+// more to take the weights (capped scores stay in TMEM in between).
+template <typename T, int G, int RULE = kNoRule>
 __global__ void __launch_bounds__(THREADS2, 1)
     decode_mq_kernel(const MqParams p, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
@@ -487,6 +487,32 @@ __global__ void __launch_bounds__(THREADS2, 1)
             RULE ? min(row_hi - tile0, n_valid - 1) : row_valid ? min(pos - tile0, n_valid - 1) : -1;
         const int lo_c = RULE ? row_lo - tile0 : 0;                      // first key column
         const bool open = __all_sync(FULL, col0 + 63 <= lim && (!RULE || col0 >= lo_c));
+        // RULE: chunk c's 32 raw scores to finished ones plus `add` (masked: -inf).
+        // Left of every row's own position the bias is linear in the key: two
+        // FMAs per score; chunks that are open need no mask.
+        const bool left = RULE && __all_sync(FULL, tile0 + col0 + 63 <= pos);
+        auto finish = [&](int c, float* sv, float add) {
+          const float d0 = static_cast<float>(pos - tile0 - col0 - c * 32);
+          if (open && left) {
+            const float b0 = fmaf(-slope, d0, add);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float bias = fmaf(slope, static_cast<float>(j), b0);
+              if constexpr (RULE == kRuleCapped)
+                sv[j] = rule_cap<RULE>(p.rule.cap_log2, sv[j] * p.scale_log2) + bias;
+              else
+                sv[j] = fmaf(sv[j], p.scale_log2, bias);
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const int col = col0 + c * 32 + j;
+              const float x = rule_score<RULE>(p.rule, sv[j] * p.scale_log2, slope,
+                                               fabsf(d0 - static_cast<float>(j)));
+              sv[j] = open || (col >= lo_c && col <= lim) ? x + add : -INFINITY;
+            }
+          }
+        };
         // pass 1: the row's maximum over this half (raw scores when open)
         float pm[8];
 #pragma unroll
@@ -498,17 +524,12 @@ __global__ void __launch_bounds__(THREADS2, 1)
           else
 #pragma unroll
             for (int j = 0; j < 32; ++j) sv[j] = 0.f;
-          if constexpr (RULE) {
-            const float d0 = static_cast<float>(pos - tile0 - col0 - c * 32);
+          if constexpr (RULE != kNoRule) {
+            finish(c, sv, 0.f);
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int col = col0 + c * 32 + j;
-              const float x =
-                  rule_score(p.rule, sv[j] * p.scale_log2, slope, fabsf(d0 - static_cast<float>(j)));
-              sv[j] = open || (col >= lo_c && col <= lim) ? x : -INFINITY;
-              pm[j & 7] = fmaxf(pm[j & 7], sv[j]);
-            }
-            tmem_st32(s_col + c * 32, sv);
+            for (int j = 0; j < 32; ++j) pm[j & 7] = fmaxf(pm[j & 7], sv[j]);
+            // capped scores cost two special-function results: kept for pass 2
+            if constexpr (RULE == kRuleCapped) tmem_st32(s_col + c * 32, sv);
             continue;
           }
 #pragma unroll
@@ -555,12 +576,16 @@ __global__ void __launch_bounds__(THREADS2, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) sv[j] = 0.f;
           uint32_t w[16];
+          if constexpr (RULE == kRuleOpen) finish(c, sv, neg_m);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j0 = 2 * e, j1 = 2 * e + 1;
             float p0, p1;
-            if (RULE) {
-              p0 = ex2_approx(sv[j0] + neg_m);      // masked: 2^-inf = 0
+            if constexpr (RULE == kRuleOpen) {
+              p0 = ex2_approx(sv[j0]);              // masked: 2^-inf = 0
+              p1 = ex2_approx(sv[j1]);
+            } else if constexpr (RULE == kRuleCapped) {
+              p0 = ex2_approx(sv[j0] + neg_m);
               p1 = ex2_approx(sv[j1] + neg_m);
             } else if (open) {
               p0 = ex2_approx(fmaf(sv[j0], p.scale_log2, neg_m));
@@ -726,7 +751,7 @@ __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReducePar
   for (int e = 0; e < DPL; ++e) dst[e] = Elem<T>::from_float(acc[e] * inv);
 }
 
-template <typename T, int G, bool RULE>
+template <typename T, int G, int RULE>
 cudaError_t launch_mq_t(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
   auto kern = decode_mq_kernel<T, G, RULE>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
@@ -793,7 +818,7 @@ cudaError_t launch_mq_reduce_t(const MqArgs& a, cudaStream_t stream) {
   return launch_overlapped(decode_mq_reduce_kernel<T>, dim3(grid), dim3(128), 0, stream, p);
 }
 
-template <typename T, bool RULE>
+template <typename T, int RULE>
 cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
   switch (a.Hq / a.Hkv) {
     case 1: return launch_mq_t<T, 1, RULE>(a, status, stream);
@@ -808,11 +833,18 @@ cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stre
 
 int launch_decode_mq(const MqArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (a.has_rule)
-    return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16, true>(a, status, st)
-                              : launch_mq_g<__half, true>(a, status, st);
-  return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16, false>(a, status, st)
-                            : launch_mq_g<__half, false>(a, status, st);
+  const bool bf = a.dtype == PA_BF16;
+  switch (rule_kind(a.has_rule, a.rule)) {
+    case kRuleOpen:
+      return bf ? launch_mq_g<__nv_bfloat16, kRuleOpen>(a, status, st)
+                : launch_mq_g<__half, kRuleOpen>(a, status, st);
+    case kRuleCapped:
+      return bf ? launch_mq_g<__nv_bfloat16, kRuleCapped>(a, status, st)
+                : launch_mq_g<__half, kRuleCapped>(a, status, st);
+    default:
+      return bf ? launch_mq_g<__nv_bfloat16, kNoRule>(a, status, st)
+                : launch_mq_g<__half, kNoRule>(a, status, st);
+  }
 }
 
 int launch_decode_mq_reduce(const MqArgs& a, void* stream) {

@@ -211,7 +211,7 @@ struct TcParams {
 // taken from the block of the first key that any of its query tokens sees (the
 // shift of a grouped decode, found here), up to the last one; a column's own
 // limits are then relative to that block.
-template <typename T, int G, int NQ = 1, int NP = 16, int CTAS = 2, bool RULE = false>
+template <typename T, int G, int NQ = 1, int NP = 16, int CTAS = 2, int RULE = kNoRule>
 __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
     decode_partition_tc_kernel(const TcParams p, const __grid_constant__ CUtensorMap tmap_k,
                                const __grid_constant__ CUtensorMap tmap_v) {
@@ -642,7 +642,7 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
         if constexpr (RULE) {
           const int u = h / G, j = start + i * TOK + r;
           ok_h = j >= lo_u[u] && j <= hi_u[u];
-          const float x = rule_score(p.rule, sv[h] * p.scale_log2, slope[h % G],
+          const float x = rule_score<RULE>(p.rule, sv[h] * p.scale_log2, slope[h % G],
                                      fabsf(static_cast<float>(pos_u[u] - j)));
           s[h] = ok_h ? x : -INFINITY;
           need |= s[h] > m_run[h] + RESCALE_THRESHOLD;
@@ -752,7 +752,7 @@ __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
 
 // ---- host side ----
 
-template <typename T, int G, bool RULE = false>
+template <typename T, int G, int RULE = kNoRule>
 cudaError_t launch_tc_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
   const int ppc = tc_parts_per_cta(a);
   auto kern = decode_partition_tc_kernel<T, G, 1, 16, 2, RULE>;
@@ -934,7 +934,7 @@ bool tmap_available() { return encode_fn() != nullptr; }
 
 namespace {
 
-template <typename T, int G, int NQ, int NP, bool RULE>
+template <typename T, int G, int NQ, int NP, int RULE>
 cudaError_t launch_tcq_t(const MqArgs& m, unsigned int* status, cudaStream_t stream) {
   const int q_groups = (m.max_query_len + NQ - 1) / NQ;
   const int ppc = tc_parts_per_cta(static_cast<int64_t>(m.num_seqs) * q_groups * m.Hkv,
@@ -989,7 +989,7 @@ cudaError_t launch_tcq_t(const MqArgs& m, unsigned int* status, cudaStream_t str
 // Query tokens per CTA (tc_query_tokens_per_cta): up to 16 columns on the
 // N = 16 kernel, else 32 columns on the N = 32 kernel, so 4 tokens at G = 8
 // (or 8 at G = 4) share one read of the sequence's K/V.
-template <typename T, bool RULE>
+template <typename T, int RULE>
 cudaError_t launch_tcq_g(const MqArgs& m, unsigned int* status, cudaStream_t stream) {
   const int G = m.Hq / m.Hkv;
   const int nq = tc_query_tokens_per_cta(G, m.max_query_len);
@@ -1016,11 +1016,18 @@ bool decode_mq_tc_supported(const MqArgs& m) {
 
 int launch_decode_mq_tc(const MqArgs& m, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (m.has_rule)
-    return m.dtype == PA_BF16 ? launch_tcq_g<__nv_bfloat16, true>(m, status, st)
-                              : launch_tcq_g<__half, true>(m, status, st);
-  return m.dtype == PA_BF16 ? launch_tcq_g<__nv_bfloat16, false>(m, status, st)
-                            : launch_tcq_g<__half, false>(m, status, st);
+  const bool bf = m.dtype == PA_BF16;
+  switch (rule_kind(m.has_rule, m.rule)) {
+    case kRuleOpen:
+      return bf ? launch_tcq_g<__nv_bfloat16, kRuleOpen>(m, status, st)
+                : launch_tcq_g<__half, kRuleOpen>(m, status, st);
+    case kRuleCapped:
+      return bf ? launch_tcq_g<__nv_bfloat16, kRuleCapped>(m, status, st)
+                : launch_tcq_g<__half, kRuleCapped>(m, status, st);
+    default:
+      return bf ? launch_tcq_g<__nv_bfloat16, kNoRule>(m, status, st)
+                : launch_tcq_g<__half, kNoRule>(m, status, st);
+  }
 }
 
 bool decode_tc_supported(const DecodeArgs& a) {
@@ -1079,12 +1086,20 @@ int launch_decode_group_tc(const DecodeArgs& a, unsigned int* status, void* stre
 int launch_decode_partitions_tc(const DecodeArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int G = a.Hq / a.Hkv;
-  if (a.has_rule) {
+  const Rule rule = rule_kind(a.has_rule, a.rule);
+  if (rule == kRuleOpen) {
     if (a.dtype == PA_BF16)
-      return G == 8 ? launch_tc_t<__nv_bfloat16, 8, true>(a, status, st)
-                    : launch_tc_t<__nv_bfloat16, 4, true>(a, status, st);
-    return G == 8 ? launch_tc_t<__half, 8, true>(a, status, st)
-                  : launch_tc_t<__half, 4, true>(a, status, st);
+      return G == 8 ? launch_tc_t<__nv_bfloat16, 8, kRuleOpen>(a, status, st)
+                    : launch_tc_t<__nv_bfloat16, 4, kRuleOpen>(a, status, st);
+    return G == 8 ? launch_tc_t<__half, 8, kRuleOpen>(a, status, st)
+                  : launch_tc_t<__half, 4, kRuleOpen>(a, status, st);
+  }
+  if (rule == kRuleCapped) {
+    if (a.dtype == PA_BF16)
+      return G == 8 ? launch_tc_t<__nv_bfloat16, 8, kRuleCapped>(a, status, st)
+                    : launch_tc_t<__nv_bfloat16, 4, kRuleCapped>(a, status, st);
+    return G == 8 ? launch_tc_t<__half, 8, kRuleCapped>(a, status, st)
+                  : launch_tc_t<__half, 4, kRuleCapped>(a, status, st);
   }
   if (a.dtype == PA_BF16) {
     return G == 8 ? launch_tc_t<__nv_bfloat16, 8>(a, status, st)

