@@ -41,6 +41,7 @@
 #include <type_traits>
 
 #include "pa_device.cuh"
+#include "mq_common.cuh"
 #include "pa_internal.h"
 #include "pa_rule.cuh"
 #include "tc_common.cuh"
@@ -50,19 +51,10 @@ namespace pa {
 namespace {
 
 using namespace tc;
+using namespace mq;
 
 constexpr unsigned FULL = 0xffffffffu;
-constexpr int TOK = 128;                   // keys per tile
-constexpr int MR = 128;                    // query rows per query block
-constexpr int DH = 128;
 constexpr int SLOTS = 3;
-constexpr int SLOT_BYTES = TOK * 256;      // K or V tile (as in decode_tc.cu): 32 KB
-constexpr int GROUP_BYTES = 2048;
-constexpr int HALF_OFF = 1024;
-constexpr int OPA_BYTES = MR * 256;        // a 128 x 128 16-bit row-major operand: 32 KB
-constexpr int OPA_HALF = MR * 128;         // its second 64-column half
-constexpr int TMEM_COLS = 512;
-constexpr float RESCALE_THRESHOLD = 8.0f;
 
 // ---- the query-major kernel with two query tiles per CTA (decode_mq_kernel) ----
 // TMEM: S of tile X at X * 128, O of tile X at 256 + X * 128; P of tile X
@@ -80,101 +72,6 @@ constexpr int SMEM2_BYTES = SMEM2_USED + 1024;
 static_assert(SMEM2_BYTES <= 227 * 1024, "shared memory");
 static_assert(NT == 2, "two query tiles: TMEM holds 2 x (S, O) of 128 columns");
 
-// kind::f16 instruction descriptor, fp32 accumulation, M = 128, N = 128;
-// A K-major; B K-major (S) or MN-major (O).
-template <typename T>
-__device__ __forceinline__ constexpr uint32_t idesc_mq(bool b_mn_major) {
-  constexpr uint32_t fmt = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-  return (1u << 4) | (fmt << 7) | (fmt << 10) | ((b_mn_major ? 1u : 0u) << 16) |
-         ((uint32_t)(128 >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
-  uint32_t r[32];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,"
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float* v) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-      "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n\t"
-      "tcgen05.wait::st.sync.aligned;" ::"r"(taddr),
-      "r"(__float_as_uint(v[0])), "r"(__float_as_uint(v[1])), "r"(__float_as_uint(v[2])),
-      "r"(__float_as_uint(v[3])), "r"(__float_as_uint(v[4])), "r"(__float_as_uint(v[5])),
-      "r"(__float_as_uint(v[6])), "r"(__float_as_uint(v[7])), "r"(__float_as_uint(v[8])),
-      "r"(__float_as_uint(v[9])), "r"(__float_as_uint(v[10])), "r"(__float_as_uint(v[11])),
-      "r"(__float_as_uint(v[12])), "r"(__float_as_uint(v[13])), "r"(__float_as_uint(v[14])),
-      "r"(__float_as_uint(v[15])), "r"(__float_as_uint(v[16])), "r"(__float_as_uint(v[17])),
-      "r"(__float_as_uint(v[18])), "r"(__float_as_uint(v[19])), "r"(__float_as_uint(v[20])),
-      "r"(__float_as_uint(v[21])), "r"(__float_as_uint(v[22])), "r"(__float_as_uint(v[23])),
-      "r"(__float_as_uint(v[24])), "r"(__float_as_uint(v[25])), "r"(__float_as_uint(v[26])),
-      "r"(__float_as_uint(v[27])), "r"(__float_as_uint(v[28])), "r"(__float_as_uint(v[29])),
-      "r"(__float_as_uint(v[30])), "r"(__float_as_uint(v[31]))
-      : "memory");
-}
-
-// MMA with the A operand in TMEM (M = 128 lanes, K along the columns: two
-// 16-bit elements per 32-bit column) and B from shared memory.
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b,
-                                           uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// 16 32-bit words into 16 consecutive TMEM columns of this thread's lane.
-__device__ __forceinline__ void tmem_st16u(uint32_t taddr, const uint32_t* w) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
-      "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]),
-      "r"(w[8]), "r"(w[9]), "r"(w[10]), "r"(w[11]), "r"(w[12]), "r"(w[13]), "r"(w[14]), "r"(w[15])
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() {
-  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-}
-
-// 2^x by the SFU's approximation (relative error about 2^-22; 2^-inf = +0).
-__device__ __forceinline__ float ex2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two floats rounded to T and packed (the first in the low half), one cvt.
-template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  } else {
-    const __half2 v = __floats2half2_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&v);
-  }
-}
-
-// Byte offset of the 16-byte chunk c (elements 8c..8c+7) of row r of a
-// 128 x 128 16-bit operand stored as two 64-column halves with the 128-byte
-// swizzle (the canonical K-major layout).
-__device__ __forceinline__ uint32_t opa_chunk(int r, int c) {
-  return (c >> 3) * OPA_HALF + r * 128 + ((((c & 7) ^ (r & 7)) & 7) << 4);
-}
-
 struct MqParams {
   void* out;
   const void* q;
@@ -188,7 +85,6 @@ struct MqParams {
   int64_t max_blocks;
   int num_seqs, total_q, Hq, Hkv, num_blocks, block_size, partition_size, num_partitions;
   float scale_log2;
-  RuleParams rule;   // RULE instances (pa_decode_multi_scored)
 };
 
 // Query-major multi-query kernel with two query tiles per CTA: a CTA serves
@@ -203,12 +99,7 @@ struct MqParams {
 // straight from TMEM, so no shared memory holds P.  Warps 0 and 1: producer
 // and MMA issuer; warps 2 + 8X .. 9 + 8X: tile X.  Shared memory: the K/V ring
 // and the two Q tiles (~167 KB); all 512 TMEM columns.
-// RULE: capped, distance-biased, windowed scores (pa_rule.cuh).  The CTA's keys
-// run from the block of the first key that any of its query tokens sees
-// (positions below are counted from there) to the last one; the first pass
-// over a tile's scores applies the rule to find the maximum, the second once
-// more to take the weights (capped scores stay in TMEM in between).
-template <typename T, int G, int RULE = kNoRule>
+template <typename T, int G>
 __global__ void __launch_bounds__(THREADS2, 1)
     decode_mq_kernel(const MqParams p, const __grid_constant__ CUtensorMap tmap_k,
                       const __grid_constant__ CUtensorMap tmap_v) {
@@ -243,7 +134,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int P = p.partition_size;
   int64_t cap = p.max_blocks * p.block_size;
   const int64_t grid_cap = static_cast<int64_t>(p.num_partitions) * P;
-  if (!RULE) cap = cap < grid_cap ? cap : grid_cap;
+  cap = cap < grid_cap ? cap : grid_cap;
   if (L < 0 || L > cap || Qb < 0 || Qb > L || q0 < 0 || q0 + Qb > p.total_q) {
     if (threadIdx.x == 0 && pair == 0 && part == 0 && g == 0) atomicOr(p.status, PA_DEVERR_CONTEXT);
     return;
@@ -253,29 +144,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int qb0 = pair * NT;                        // the CTA's first query block
   if (qb0 * QB >= Qb) return;                       // no query tokens here
   const int i_last = min(Qb, (qb0 + NT) * QB) - 1;  // the CTA's last query token
-  int pmax = L - Qb + i_last;                       // its position: the last key needed
-  int shift = 0, first = 0;   // RULE: tokens before the first key's block, and from there to it
-  if constexpr (RULE) {
-    int lo, hi;
-    rule_span(p.rule, b, q0, L - Qb, L, qb0 * QB, i_last + 1, lo, hi);
-    if (lo > hi) {                                  // nothing is seen: zero rows
-      if (part == 0) {
-        const int i0 = qb0 * QB;
-        for (int i = threadIdx.x; i < (i_last + 1 - i0) * G * DH; i += THREADS2) {
-          const int64_t hq = (static_cast<int64_t>(q0) + i0 + i / (G * DH)) * p.Hq + g * G + i / DH % G;
-          static_cast<T*>(p.out)[hq * DH + i % DH] = Elem<T>::from_float(0.f);
-        }
-      }
-      return;
-    }
-    shift = lo / p.block_size * p.block_size;
-    first = lo - shift;
-    pmax = hi - shift;
-    if (pmax >= grid_cap) {                         // a context beyond max_context_len
-      if (threadIdx.x == 0 && part == 0 && g == 0) atomicOr(p.status, PA_DEVERR_CONTEXT);
-      return;
-    }
-  }
+  const int pmax = L - Qb + i_last;                 // its position: the last key needed
   const int kstart = part * P;
   if (kstart > pmax) return;
   const int kend = min(kstart + P, pmax + 1);
@@ -286,7 +155,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int bpt = TOK / bs;
   const int first_blk = kstart / bs;
   const int last_blk = (kend + bs - 1) / bs;
-  const int32_t* trow = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + shift / bs;
+  const int32_t* trow = p.block_tables + static_cast<int64_t>(b) * p.max_blocks;
   if (threadIdx.x == 0) {
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&ring_full[s], 1);
@@ -367,18 +236,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
   const int qtok = (qb0 + X) * QB + il;             // query token of the row within the sequence
   const bool row_valid = warp >= 2 && qtok < Qb;
   const int64_t t = static_cast<int64_t>(q0) + qtok;
-  const int pos = L - Qb + qtok - shift;
-  // RULE: the keys that the row sees, and its head's slope in base 2
-  int row_lo = 0, row_hi = -1;
-  float slope = 0.f;
-  if constexpr (RULE) {
-    if (row_valid) {
-      rule_limits(p.rule, b, t, L - Qb + qtok, L, row_lo, row_hi);
-      row_lo -= shift;
-      row_hi -= shift;
-      if (p.rule.slopes != nullptr) slope = __ldcg(p.rule.slopes + g * G + hl) * kLog2e;
-    }
-  }
+  const int pos = L - Qb + qtok;
   const int pair_bar = 3 + X * 4 + quad;            // named barrier of this row's two threads
 
   if (warp >= 2) {
@@ -483,36 +341,8 @@ __global__ void __launch_bounds__(THREADS2, 1)
       wait(&s_full[X], i & 1);
       tc_fence_after();
       if (warp_active) {
-        const int lim =   // last key column
-            RULE ? min(row_hi - tile0, n_valid - 1) : row_valid ? min(pos - tile0, n_valid - 1) : -1;
-        const int lo_c = RULE ? row_lo - tile0 : 0;                      // first key column
-        const bool open = __all_sync(FULL, col0 + 63 <= lim && (!RULE || col0 >= lo_c));
-        // RULE: chunk c's 32 raw scores to finished ones plus `add` (masked: -inf).
-        // Left of every row's own position the bias is linear in the key: two
-        // FMAs per score; chunks that are open need no mask.
-        const bool left = RULE && __all_sync(FULL, tile0 + col0 + 63 <= pos);
-        auto finish = [&](int c, float* sv, float add) {
-          const float d0 = static_cast<float>(pos - tile0 - col0 - c * 32);
-          if (open && left) {
-            const float b0 = fmaf(-slope, d0, add);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float bias = fmaf(slope, static_cast<float>(j), b0);
-              if constexpr (RULE == kRuleCapped)
-                sv[j] = rule_cap<RULE>(p.rule.cap_log2, sv[j] * p.scale_log2) + bias;
-              else
-                sv[j] = fmaf(sv[j], p.scale_log2, bias);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const int col = col0 + c * 32 + j;
-              const float x = rule_score<RULE>(p.rule, sv[j] * p.scale_log2, slope,
-                                               fabsf(d0 - static_cast<float>(j)));
-              sv[j] = open || (col >= lo_c && col <= lim) ? x + add : -INFINITY;
-            }
-          }
-        };
+        const int lim = row_valid ? min(pos - tile0, n_valid - 1) : -1;  // last key column
+        const bool open = __all_sync(FULL, col0 + 63 <= lim);
         // pass 1: the row's maximum over this half (raw scores when open)
         float pm[8];
 #pragma unroll
@@ -524,14 +354,6 @@ __global__ void __launch_bounds__(THREADS2, 1)
           else
 #pragma unroll
             for (int j = 0; j < 32; ++j) sv[j] = 0.f;
-          if constexpr (RULE != kNoRule) {
-            finish(c, sv, 0.f);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) pm[j & 7] = fmaxf(pm[j & 7], sv[j]);
-            // capped scores cost two special-function results: kept for pass 2
-            if constexpr (RULE == kRuleCapped) tmem_st32(s_col + c * 32, sv);
-            continue;
-          }
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             const float x = open ? sv[j] : (col0 + c * 32 + j <= lim ? sv[j] : -INFINITY);
@@ -540,7 +362,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
         }
         float tmax = fmaxf(fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3])),
                            fmaxf(fmaxf(pm[4], pm[5]), fmaxf(pm[6], pm[7])));
-        if (!RULE) tmax = tmax == -INFINITY ? tmax : tmax * p.scale_log2;
+        tmax = tmax == -INFINITY ? tmax : tmax * p.scale_log2;
         rmax[(((i & 1) * NT + X) * 2 + half) * MR + r] = tmax;
         named_sync(pair_bar, 64);
         tmax = fmaxf(tmax, rmax[(((i & 1) * NT + X) * 2 + (half ^ 1)) * MR + r]);
@@ -564,7 +386,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
           }
         }
         // pass 2: P = 2^(scale * s - m) into the first 32 of my S columns
-        const float neg_m = RULE && m_run == -INFINITY ? 0.f : -m_run;
+        const float neg_m = -m_run;
         float ps[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) ps[k] = 0.f;
@@ -576,18 +398,11 @@ __global__ void __launch_bounds__(THREADS2, 1)
 #pragma unroll
             for (int j = 0; j < 32; ++j) sv[j] = 0.f;
           uint32_t w[16];
-          if constexpr (RULE == kRuleOpen) finish(c, sv, neg_m);
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int j0 = 2 * e, j1 = 2 * e + 1;
             float p0, p1;
-            if constexpr (RULE == kRuleOpen) {
-              p0 = ex2_approx(sv[j0]);              // masked: 2^-inf = 0
-              p1 = ex2_approx(sv[j1]);
-            } else if constexpr (RULE == kRuleCapped) {
-              p0 = ex2_approx(sv[j0] + neg_m);
-              p1 = ex2_approx(sv[j1] + neg_m);
-            } else if (open) {
+            if (open) {
               p0 = ex2_approx(fmaf(sv[j0], p.scale_log2, neg_m));
               p1 = ex2_approx(fmaf(sv[j1], p.scale_log2, neg_m));
             } else {
@@ -611,12 +426,11 @@ __global__ void __launch_bounds__(THREADS2, 1)
         tmem_st16u(s_col, z);
         tmem_st16u(s_col + 16, z);
       }
-      const int n_first = RULE ? first - tile0 : 0;   // > 0 in the first tile only
-      if (X == 0 && (n_valid < TOK || (RULE && n_first > 0))) {
+      if (X == 0 && n_valid < TOK) {
         // the last tile: zero the V rows of keys past the range (this thread
         // its 64-dim half of row r), so that whatever they hold adds 0 to O
         const int u = 2 * i + 1, s_ = u % SLOTS;
-        if (wait(&ring_full[s_], (u / SLOTS) & 1) && (r >= n_valid || (RULE && r < n_first))) {
+        if (wait(&ring_full[s_], (u / SLOTS) & 1) && r >= n_valid) {
           uint8_t* row = ring + s_ * SLOT_BYTES + (r >> 3) * GROUP_BYTES + (r & 7) * 128 + half * HALF_OFF;
 #pragma unroll
           for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0, 0, 0, 0);
@@ -641,7 +455,7 @@ __global__ void __launch_bounds__(THREADS2, 1)
       tmem_ld32(o_col + c * 32, o);
       if (ok && row_valid) {
         if (single) {
-          const float inv = RULE && l_sum == 0.f ? 0.f : 1.f / l_sum;
+          const float inv = 1.f / l_sum;
           T* dst = static_cast<T*>(p.out) + hq * DH + col0 + c * 32;
 #pragma unroll
           for (int j = 0; j < 32; j += 8) {
@@ -751,9 +565,9 @@ __global__ void __launch_bounds__(128) decode_mq_reduce_kernel(const MqReducePar
   for (int e = 0; e < DPL; ++e) dst[e] = Elem<T>::from_float(acc[e] * inv);
 }
 
-template <typename T, int G, int RULE>
+template <typename T, int G>
 cudaError_t launch_mq_t(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
-  auto kern = decode_mq_kernel<T, G, RULE>;
+  auto kern = decode_mq_kernel<T, G>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM2_BYTES);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
@@ -785,8 +599,6 @@ cudaError_t launch_mq_t(const MqArgs& a, unsigned int* status, cudaStream_t stre
   p.partition_size = a.partition_size;
   p.num_partitions = a.num_partitions;
   p.scale_log2 = a.scale * 1.4426950408889634f;
-  p.rule = make_rule(a.rule, a.scale);
-  if (RULE) p.scale_log2 = p.rule.scale;
   const int qblocks = (a.max_query_len + MR / G - 1) / (MR / G);
   const int pairs = (qblocks + NT - 1) / NT;
   dim3 grid(a.num_seqs, a.Hkv, pairs * a.num_partitions);
@@ -818,13 +630,13 @@ cudaError_t launch_mq_reduce_t(const MqArgs& a, cudaStream_t stream) {
   return launch_overlapped(decode_mq_reduce_kernel<T>, dim3(grid), dim3(128), 0, stream, p);
 }
 
-template <typename T, int RULE>
+template <typename T>
 cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
   switch (a.Hq / a.Hkv) {
-    case 1: return launch_mq_t<T, 1, RULE>(a, status, stream);
-    case 2: return launch_mq_t<T, 2, RULE>(a, status, stream);
-    case 4: return launch_mq_t<T, 4, RULE>(a, status, stream);
-    case 8: return launch_mq_t<T, 8, RULE>(a, status, stream);
+    case 1: return launch_mq_t<T, 1>(a, status, stream);
+    case 2: return launch_mq_t<T, 2>(a, status, stream);
+    case 4: return launch_mq_t<T, 4>(a, status, stream);
+    case 8: return launch_mq_t<T, 8>(a, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -832,19 +644,10 @@ cudaError_t launch_mq_g(const MqArgs& a, unsigned int* status, cudaStream_t stre
 }  // namespace
 
 int launch_decode_mq(const MqArgs& a, unsigned int* status, void* stream) {
+  if (a.has_rule) return launch_decode_mq_rule(a, status, stream);
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const bool bf = a.dtype == PA_BF16;
-  switch (rule_kind(a.has_rule, a.rule)) {
-    case kRuleOpen:
-      return bf ? launch_mq_g<__nv_bfloat16, kRuleOpen>(a, status, st)
-                : launch_mq_g<__half, kRuleOpen>(a, status, st);
-    case kRuleCapped:
-      return bf ? launch_mq_g<__nv_bfloat16, kRuleCapped>(a, status, st)
-                : launch_mq_g<__half, kRuleCapped>(a, status, st);
-    default:
-      return bf ? launch_mq_g<__nv_bfloat16, kNoRule>(a, status, st)
-                : launch_mq_g<__half, kNoRule>(a, status, st);
-  }
+  return a.dtype == PA_BF16 ? launch_mq_g<__nv_bfloat16>(a, status, st)
+                            : launch_mq_g<__half>(a, status, st);
 }
 
 int launch_decode_mq_reduce(const MqArgs& a, void* stream) {

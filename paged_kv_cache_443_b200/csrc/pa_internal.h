@@ -155,6 +155,8 @@ struct MqArgs {
 constexpr int kMqRows = 128;  // (query token, head) rows per query tile of the multi-query kernel
 constexpr int kMqTiles = 2;   // query tiles per CTA of the multi-query kernel
 int launch_decode_mq(const MqArgs& a, unsigned int* status, void* stream);
+// Its form under a score rule (decode_mq_rule.cu).
+int launch_decode_mq_rule(const MqArgs& a, unsigned int* status, void* stream);
 // Few query tokens per sequence (max_query_len * G <= 64, G = 4 or 8): the
 // token-major tcgen05 decode kernel with per-column causal limits, 16 / G query
 // tokens per CTA (decode_tc.cu).
