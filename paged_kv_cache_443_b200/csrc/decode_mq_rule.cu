@@ -12,7 +12,11 @@
 //
 // The two blocks take turns on the tensor core (S_X and O_X fill all 512 TMEM
 // columns; P_X goes back into S_X's), so a block's softmax has to be done in the
-// time of the other's two products.  Each row has ONE softmax thread, which reads its 128
+// time of the other's two products.  Tiles are taken from the last key to the
+// first: a bias that grows with distance then puts the largest scores first,
+// and the running maximum, set by the first tiles, hardly rises again (from the
+// first key on, 72 % of the tiles of the chunks below raised it and rescaled O).
+// Each row has ONE softmax thread, which reads its 128
 // scores from TMEM once and keeps them in registers: maximum, rule, exponentials
 // and sum touch nothing else, and no two threads have to agree on a row's
 // maximum (decode_mq.cu's two threads per row read S twice and meet at a barrier
@@ -20,10 +24,10 @@
 // 8 sequences, 332 GFLOP).  The commit of S_X (i) also covers O_X (i - 1), which
 // was issued before it, so a raised maximum rescales O without another wait.
 //
-// Roles (10 warps): warps 0-3 the first block's Q staging, softmax and epilogue,
+// Roles (12 warps): warps 0-3 the first block's Q staging, softmax and epilogue,
 // warps 4-7 the second's, warp 8 TMA producer, warp 9 TMEM owner and MMA
-// issuer.  A ring of four K/V tiles and the two Q blocks, 193 KB of shared
-// memory: one CTA per SM, up to 200 registers per thread.  The CTAs of one kv
+// issuer (its warpgroup hands its registers to the softmax).  A ring of four K/V
+// tiles and the two Q blocks, 193 KB of shared memory: one CTA per SM.  The CTAs of one kv
 // head's runs are neighbours in the grid and read its K/V from L2.  Every wait
 // is bounded; block ids outside the pool are skipped and flagged; inconsistent
 // query offsets are flagged (PA_DEVERR_CONTEXT) and their sequence skipped.
@@ -48,7 +52,7 @@ using namespace mq;
 constexpr unsigned FULL = 0xffffffffu;
 constexpr int NT = kMqTiles;                    // query blocks per CTA
 constexpr int SLOTS = 4;
-constexpr int THREADS = NT * 128 + 64;
+constexpr int THREADS = NT * 128 + 128;       // two softmax warpgroups; producer, MMA, two idle
 constexpr int OFF_Q = SLOTS * SLOT_BYTES;
 constexpr int OFF_BAR = OFF_Q + NT * OPA_BYTES;
 constexpr int NBARS = 2 * SLOTS + 3 * NT + 1;   // ring full/empty, s_full, p_full, o_full, q_ready
@@ -73,24 +77,32 @@ struct Params {
 };
 
 // Pairs of fp32 in one instruction.
-__device__ __forceinline__ void mul2(float& a, float& b, float m) {
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(m));
+__device__ __forceinline__ void add2(float& x, float& y, float a, float b, float c, float d) {
+  asm("{\n\t.reg .b64 u, v;\n\tmov.b64 u, {%2, %3};\n\tmov.b64 v, {%4, %5};\n\t"
+      "add.rn.f32x2 u, u, v;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "=f"(x), "=f"(y)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
 }
-__device__ __forceinline__ void add2(float& a, float& b, float c, float d) {
-  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %3};\n\t"
-      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a), "+f"(b)
-      : "f"(c), "f"(d));
-}
-// (a, b) = (a, b) * m + (c, d)
-__device__ __forceinline__ void fma2(float& a, float& b, float m, float c, float d) {
-  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%0, %1};\n\tmov.b64 y, {%2, %2};\n\t"
-      "mov.b64 z, {%3, %4};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}"
-      : "+f"(a), "+f"(b)
+// (x, y) = (x, y) * m + (c, d)
+__device__ __forceinline__ void fma2(float& x, float& y, float m, float c, float d) {
+  asm("{\n\t.reg .b64 u, v, w;\n\tmov.b64 u, {%0, %1};\n\tmov.b64 v, {%2, %2};\n\t"
+      "mov.b64 w, {%3, %4};\n\tfma.rn.f32x2 u, u, v, w;\n\tmov.b64 {%0, %1}, u;\n\t}"
+      : "+f"(x), "+f"(y)
       : "f"(m), "f"(c), "f"(d));
+}
+
+// Register shares: the softmax warpgroups take what the producer's and the MMA
+// issuer's give up (launch: 384 threads of 168; 2 * 128 * 224 + 128 * 40 = 62464
+// of its 64512).
+constexpr int REGS_SOFTMAX = 224, REGS_OTHER = 40;
+static_assert(NT * 128 * REGS_SOFTMAX + 128 * REGS_OTHER <= 168 * THREADS, "register shares");
+template <int N>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // 32 TMEM columns of this thread's lane, without waiting for them.
@@ -115,18 +127,20 @@ __device__ __forceinline__ void hold(float* v, int n) {
   for (int i = 0; i < n; ++i) asm volatile("" : "+f"(v[i]));
 }
 
-// The 128 raw scores of a row to finished ones (base 2).  open: the row sees
-// every key of the tile; left: none lies behind the row's own position, so that
-// the bias is linear in the key (8 keys share a base, one FMA pair per two).
+// The 128 raw scores of a row to finished ones (base 2) plus `add`.  open: the
+// row sees every key of the tile; left: none lies behind the row's own position,
+// so that the bias is linear in the key (8 keys share a base; one add and one
+// FMA per two scores).
 template <int RULE, bool SLOPES>
-__device__ __forceinline__ void finish_scores(const Params& p, float* s, bool open, bool left,
-                                              int pos_c, int lo_c, int hi_c, float slope) {
+__device__ __forceinline__ void finish_scores(const Params& p, float* s, float add, bool open,
+                                              bool left, int pos_c, int lo_c, int hi_c,
+                                              float slope) {
   if constexpr (RULE == kRuleCapped) {
 #pragma unroll
     for (int j = 0; j < TOK; ++j) s[j] = rule_cap<RULE>(p.rule.cap_log2, s[j] * p.rule.scale);
   }
+  const float scale = RULE == kRuleCapped ? 1.f : p.rule.scale;
   if constexpr (SLOPES) {
-    const float scale = RULE == kRuleCapped ? 1.f : p.rule.scale;
     const float d0 = static_cast<float>(pos_c);          // the row's own column
     if (left) {
       float step[8];
@@ -134,22 +148,22 @@ __device__ __forceinline__ void finish_scores(const Params& p, float* s, bool op
       for (int e = 0; e < 8; ++e) step[e] = slope * static_cast<float>(e);
 #pragma unroll
       for (int j = 0; j < TOK; j += 8) {
-        const float base = slope * (static_cast<float>(j) - d0);
+        const float base = fmaf(slope, static_cast<float>(j) - d0, add);
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-          float b0 = step[e], b1 = step[e + 1];
-          add2(b0, b1, base, base);
+          float b0, b1;
+          add2(b0, b1, step[e], step[e + 1], base, base);
           fma2(s[j + e], s[j + e + 1], scale, b0, b1);
         }
       }
     } else {
 #pragma unroll
       for (int j = 0; j < TOK; ++j)
-        s[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), s[j] * scale);
+        s[j] = fmaf(-slope, fabsf(d0 - static_cast<float>(j)), fmaf(s[j], scale, add));
     }
-  } else if constexpr (RULE != kRuleCapped) {
+  } else {
 #pragma unroll
-    for (int j = 0; j < TOK; j += 2) mul2(s[j], s[j + 1], p.rule.scale);
+    for (int j = 0; j < TOK; j += 2) fma2(s[j], s[j + 1], scale, add, add);
   }
   if (!open) {
 #pragma unroll
@@ -265,19 +279,20 @@ __global__ void __launch_bounds__(THREADS, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
-
+  if (warp >= 4 * NT) {
+  fewer_registers<REGS_OTHER>();
   if (warp == 4 * NT) {
     // ================= producer =================
     const int row_stride = p.Hkv * bs;
     bool ok = true;
     int issued = 0;
     auto table = [&](int i) {
-      const int b0 = first_blk + i * bpt;
+      const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
       return (i < n_tiles && lane < min(bpt, last_blk - b0)) ? __ldg(trow + b0 + lane) : -1;
     };
     int pb_next = table(0);
     for (int i = 0; i < n_tiles && ok; ++i) {
-      const int b0 = first_blk + i * bpt;
+      const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
       const int nb = min(bpt, last_blk - b0);
       const int pb = pb_next;
       pb_next = table(i + 1);
@@ -306,10 +321,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int u = issued - SLOTS < 0 ? 0 : issued - SLOTS; u < issued; ++u)
         mbar_wait(&ring_full[u % SLOTS], (u / SLOTS) & 1, p.status);
     }
-    return;
-  }
-
-  if (warp == 4 * NT + 1) {
+  } else if (warp == 4 * NT + 1) {
     // ================= MMA issuer =================
     if (lane == 0) {
       const uint32_t id_s = idesc_mq<T>(false);
@@ -374,7 +386,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
     }
     __syncwarp();
+    // every softmax warp is done with TMEM
+    named_sync(1, NT * 128 + 32);
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(TMEM_COLS)
+                 : "memory");
+  }
   } else {
+    more_registers<REGS_SOFTMAX>();
     // ================= softmax: thread of block X, row r (its TMEM lane) =================
     const int X = warp >> 2;
     const int r = (warp & 3) * 32 + lane;
@@ -417,7 +437,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       return ok;
     };
     for (int i = 0; i < n_tiles; ++i) {
-      const int tile0 = kstart + i * TOK;
+      const int tile0 = kstart + (n_tiles - 1 - i) * TOK;
       const int n_valid = min(TOK, kend - tile0);
       const bool have = wait(&s_full[X], i & 1);
       tc_fence_after();
@@ -430,17 +450,23 @@ __global__ void __launch_bounds__(THREADS, 1)
         const int lo_c = row_lo - tile0, hi_c = min(row_hi - tile0, n_valid - 1);
         const bool open = __all_sync(FULL, lo_c <= 0 && hi_c >= TOK - 1);
         const bool left = __all_sync(FULL, pos - tile0 >= TOK - 1);
-        finish_scores<RULE, SLOPES>(p, s, open, left, pos - tile0, lo_c, hi_c, slope);
+        // scores relative to the running maximum (0 before the first): with no
+        // raise, which is rare, they are the exponents as they stand
+        const float m_old = m_run == -INFINITY ? 0.f : m_run;
+        finish_scores<RULE, SLOPES>(p, s, -m_old, open, left, pos - tile0, lo_c, hi_c, slope);
         float pm[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int j = 4; j + 1 < TOK; j += 2)
           pm[(j >> 1) & 3] = fmaxf(fmaxf(pm[(j >> 1) & 3], s[j]), s[j + 1]);
-        const float tmax = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-        if (__any_sync(FULL, tmax > m_run + RESCALE_THRESHOLD)) {
-          const float mnew = fmaxf(m_run, tmax);
-          const float alpha = (m_run == -INFINITY) ? 0.f : ex2_approx(m_run - mnew);
-          m_run = mnew;
+        const float rise = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        if (__any_sync(FULL, m_run == -INFINITY ? rise > -INFINITY : rise > RESCALE_THRESHOLD)) {
+          // every row of the warp to its maximum so far
+          const float up = m_run == -INFINITY ? (rise == -INFINITY ? 0.f : rise) : fmaxf(rise, 0.f);
+          const float alpha = m_run == -INFINITY ? 0.f : ex2_approx(-up);
+          if (m_run != -INFINITY || rise > -INFINITY) m_run = m_old + up;
           l_sum *= alpha;
+#pragma unroll
+          for (int j = 0; j < TOK; j += 2) add2(s[j], s[j + 1], s[j], s[j + 1], -up, -up);
           if (i > 0) {                             // O of tiles before i is complete (see above)
 #pragma unroll 1
             for (int c = 0; c < DH / 16; ++c) {
@@ -452,18 +478,15 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
         }
-        const float neg_m = m_run == -INFINITY ? 0.f : -m_run;   // masked: 2^-inf = 0
         float ps[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int c = 0; c < TOK / 32; ++c) {
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            float a = s[32 * c + 2 * e], d = s[32 * c + 2 * e + 1];
-            add2(a, d, neg_m, neg_m);
-            a = ex2_approx(a);
-            d = ex2_approx(d);
-            add2(ps[(2 * e) & 3], ps[(2 * e + 1) & 3], a, d);
+            const float a = ex2_approx(s[32 * c + 2 * e]);   // masked: 2^-inf = 0
+            const float d = ex2_approx(s[32 * c + 2 * e + 1]);
+            add2(ps[(2 * e) & 3], ps[(2 * e + 1) & 3], ps[(2 * e) & 3], ps[(2 * e + 1) & 3], a, d);
             w[e] = pack2<T>(a, d);
           }
           tmem_st16u(s_col + c * 16, w);
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int c = 0; c < TOK / 32; ++c) tmem_st16u(s_col + c * 16, z);
       }
-      const int n_first = first - tile0;           // > 0 in the first tile only
+      const int n_first = first - tile0;           // > 0 in the sequence's first tile only
       if (X == 0 && (n_valid < TOK || n_first > 0)) {
         // zero the V rows of keys that no token of the run sees, so that
         // whatever they hold adds 0 to O (PV of both blocks waits for this)
@@ -528,16 +551,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
       }
     }
-  }
-
-  // ---- teardown: all but the producer meet, the MMA warp frees TMEM ----
-  tc_fence_before();
-  named_sync(1, THREADS - 32);
-  if (warp == 4 * NT + 1) {
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(TMEM_COLS)
-                 : "memory");
+    tc_fence_before();
+    named_sync(1, NT * 128 + 32);
   }
 }
 
