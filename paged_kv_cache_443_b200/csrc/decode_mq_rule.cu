@@ -55,7 +55,8 @@ constexpr int SLOTS = 4;
 constexpr int THREADS = NT * 128 + 128;       // two softmax warpgroups; producer, MMA, two idle
 constexpr int OFF_Q = SLOTS * SLOT_BYTES;
 constexpr int OFF_BAR = OFF_Q + NT * OPA_BYTES;
-constexpr int NBARS = 2 * SLOTS + 3 * NT + 1;   // ring full/empty, s_full, p_full, o_full, q_ready
+// ring full/empty; s_full, p_half, p_full, o_full per block; q_ready
+constexpr int NBARS = 2 * SLOTS + 4 * NT + 1;
 constexpr int OFF_TMEM = OFF_BAR + NBARS * 8;
 constexpr int SMEM_BYTES = OFF_TMEM + 16 + 1024;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory");
@@ -193,7 +194,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   uint64_t* ring_full = bars;
   uint64_t* ring_empty = bars + SLOTS;
   uint64_t* s_full = bars + 2 * SLOTS;              // [NT]
-  uint64_t* p_full = s_full + NT;                   // [NT]
+  uint64_t* p_half = s_full + NT;                   // [NT] P of the tile's first 64 keys
+  uint64_t* p_full = p_half + NT;                   // [NT] and of the rest
   uint64_t* o_full = p_full + NT;                   // [NT]
   uint64_t* q_ready = o_full + NT;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + OFF_TMEM);
@@ -260,6 +262,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int x = 0; x < NT; ++x) {
       mbar_init(&s_full[x], 1);
+      mbar_init(&p_half[x], 4);
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
     }
@@ -340,11 +343,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         mma_commit(&s_full[x]);
       };
-      auto issue_pv = [&](int x, int i) {          // O_x += P_x . V_i, P_x in TMEM
+      auto issue_pv = [&](int x, int i, int h) {   // O_x += P_x . V_i over half h's keys, P_x in TMEM
         const int s = (2 * i + 1) % SLOTS;
         const uint32_t d = tmem + 256 + x * 128;
 #pragma unroll
-        for (int k = 0; k < TOK / 16; ++k) {
+        for (int k = 4 * h; k < 4 * h + 4; ++k) {
           const uint64_t bv =
               smem_desc(ring_a + s * SLOT_BYTES + k * 2 * GROUP_BYTES, HALF_OFF, GROUP_BYTES);
           mma_f16_ts(d, tmem + x * 128 + k * 8, bv, id_o, (i > 0 || k > 0) ? 1u : 0u);
@@ -360,10 +363,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       for (int i = 0; i < n_tiles && ok; ++i) {
         const bool more = i + 1 < n_tiles;
-        ok = ring_wait(2 * i + 1) && mbar_wait(&p_full[0], i & 1, p.status);
+        ok = ring_wait(2 * i + 1) && mbar_wait(&p_half[0], i & 1, p.status);
         if (!ok) break;
         tc_fence_after();
-        issue_pv(0, i);
+        issue_pv(0, i, 0);
+        ok = mbar_wait(&p_full[0], i & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(0, i, 1);
         if (more) {
           ok = ring_wait(2 * i + 2);
           if (!ok) break;
@@ -372,10 +379,14 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           mma_commit(&o_full[0]);
         }
+        ok = mbar_wait(&p_half[1], i & 1, p.status);
+        if (!ok) break;
+        tc_fence_after();
+        issue_pv(1, i, 0);
         ok = mbar_wait(&p_full[1], i & 1, p.status);
         if (!ok) break;
         tc_fence_after();
-        issue_pv(1, i);
+        issue_pv(1, i, 1);
         mma_commit(&ring_empty[(2 * i + 1) % SLOTS]);
         if (more) {
           issue_s(1, i + 1);
@@ -436,9 +447,30 @@ __global__ void __launch_bounds__(THREADS, 1)
       ok = __all_sync(FULL, ok);
       return ok;
     };
+    auto first_half = [&]() {                       // P of the tile's first 64 keys is there
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&p_half[X]);
+    };
     for (int i = 0; i < n_tiles; ++i) {
       const int tile0 = kstart + (n_tiles - 1 - i) * TOK;
       const int n_valid = min(TOK, kend - tile0);
+      const int n_first = first - tile0;           // > 0 in the sequence's first tile only
+      if (X == 0 && (n_valid < TOK || n_first > 0)) {
+        // zero the V rows of keys that no token of the run sees, so that
+        // whatever they hold adds 0 to O (PV of both blocks waits for this)
+        const int u = 2 * i + 1, s_ = u % SLOTS;
+        if (wait(&ring_full[s_], (u / SLOTS) & 1) && (r >= n_valid || r < n_first)) {
+          uint8_t* row = ring + s_ * SLOT_BYTES + (r >> 3) * GROUP_BYTES + (r & 7) * 128;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0, 0, 0, 0);
+            *reinterpret_cast<uint4*>(row + HALF_OFF + c * 16) = make_uint4(0, 0, 0, 0);
+          }
+        }
+        fence_async_smem();
+      }
       const bool have = wait(&s_full[X], i & 1);
       tc_fence_after();
       if (warp_active && have) {
@@ -490,6 +522,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             w[e] = pack2<T>(a, d);
           }
           tmem_st16u(s_col + c * 16, w);
+          if (c == 1) first_half();
         }
         l_sum += (ps[0] + ps[1]) + (ps[2] + ps[3]);
       } else {
@@ -499,21 +532,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int e = 0; e < 16; ++e) z[e] = 0u;
 #pragma unroll
         for (int c = 0; c < TOK / 32; ++c) tmem_st16u(s_col + c * 16, z);
-      }
-      const int n_first = first - tile0;           // > 0 in the sequence's first tile only
-      if (X == 0 && (n_valid < TOK || n_first > 0)) {
-        // zero the V rows of keys that no token of the run sees, so that
-        // whatever they hold adds 0 to O (PV of both blocks waits for this)
-        const int u = 2 * i + 1, s_ = u % SLOTS;
-        if (wait(&ring_full[s_], (u / SLOTS) & 1) && (r >= n_valid || r < n_first)) {
-          uint8_t* row = ring + s_ * SLOT_BYTES + (r >> 3) * GROUP_BYTES + (r & 7) * 128;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0, 0, 0, 0);
-            *reinterpret_cast<uint4*>(row + HALF_OFF + c * 16) = make_uint4(0, 0, 0, 0);
-          }
-        }
-        fence_async_smem();
+        first_half();
       }
       tmem_wait_st();
       tc_fence_before();
