@@ -24,8 +24,8 @@
 // 8 sequences, 332 GFLOP).  The commit of S_X (i) also covers O_X (i - 1), which
 // was issued before it, so a raised maximum rescales O without another wait.
 //
-// Roles (12 warps): warps 0-3 the first block's Q staging, softmax and epilogue,
-// warps 4-7 the second's, warp 8 TMA producer, warp 9 TMEM owner and MMA
+// Roles (12 warps): warps 0-3 the first block's softmax and epilogue, warps 4-7
+// the second's, warp 8 TMA producer (Q, then the K/V tiles), warp 9 TMEM owner and MMA
 // issuer (its warpgroup hands its registers to the softmax).  A ring of four K/V
 // tiles and the two Q blocks, 193 KB of shared memory: one CTA per SM.  The CTAs of one kv
 // head's runs are neighbours in the grid and read its K/V from L2.  Every wait
@@ -184,7 +184,8 @@ __device__ __forceinline__ void finish_scores(const Params& p, float* s, float a
 template <typename T, int RULE, bool SLOPES>
 __global__ void __launch_bounds__(THREADS, 1)
     decode_mq_rule_kernel(const Params p, const __grid_constant__ CUtensorMap tmap_k,
-                          const __grid_constant__ CUtensorMap tmap_v) {
+                          const __grid_constant__ CUtensorMap tmap_v,
+                          const __grid_constant__ CUtensorMap tmap_q) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const int first_blk = kstart / bs;
   const int last_blk = (kend + bs - 1) / bs;
   const int32_t* trow = p.block_tables + static_cast<int64_t>(b) * p.max_blocks + shift / bs;
-  if (threadIdx.x == 0) {
+  if (warp == 4 * NT && lane == 0) {                // the producer
     for (int s = 0; s < SLOTS; ++s) {
       mbar_init(&ring_full[s], 1);
       mbar_init(&ring_empty[s], 1);
@@ -266,8 +267,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(&p_full[x], 4);
       mbar_init(&o_full[x], 1);
     }
-    mbar_init(q_ready, 4 * NT);
+    mbar_init(q_ready, 1);
     fence_mbar_init();
+    // Q of both blocks: row r = (token r / G, head r % G), 64 columns a box.
+    // Rows past the run's tokens hold other tokens' queries or zeros; what
+    // becomes of them is not written.
+    mbar_arrive_expect_tx(q_ready, NT * OPA_BYTES);
+#pragma unroll
+    for (int c = 0; c < 2 * NT; ++c)
+      tma_load_4d(qop + c * OPA_HALF, &tmap_q, 0, g * G, c & 1, q0 + i0 + (c >> 1) * QB, q_ready);
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_k)) : "memory");
     asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&tmap_v)) : "memory");
   }
@@ -422,20 +430,6 @@ __global__ void __launch_bounds__(THREADS, 1)
       row_hi -= shift;
       if (SLOPES && p.rule.slopes != nullptr) slope = __ldcg(p.rule.slopes + head) * kLog2e;
     }
-    {
-      // Q operand: row r = q[t][head][:], zero past the sequence's query tokens
-      const T* src = static_cast<const T*>(p.q) + (t * p.Hq + head) * DH;
-      uint4 v[DH / 8];
-#pragma unroll
-      for (int c = 0; c < DH / 8; ++c)
-        v[c] = row_valid ? __ldg(reinterpret_cast<const uint4*>(src + c * 8)) : make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int c = 0; c < DH / 8; ++c)
-        *reinterpret_cast<uint4*>(qop + X * OPA_BYTES + opa_chunk(r, c)) = v[c];
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_ready);
-    }
     const bool warp_active = __any_sync(FULL, row_valid);
     const uint32_t lane_base = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_col = tmem + lane_base + X * 128;
@@ -580,7 +574,7 @@ cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream)
   auto kern = decode_mq_rule_kernel<T, RULE, SLOPES>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
-  CUtensorMap mk, mv;
+  CUtensorMap mk, mv, mq;
   const int64_t groups = static_cast<int64_t>(a.num_blocks) * a.Hkv * a.block_size / 8;
   const int64_t dims[4] = {64, 8, 2, groups};
   const int64_t strides[3] = {DH * 2, 128, 8 * DH * 2};
@@ -588,6 +582,13 @@ cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream)
   if (!make_tmap(&mk, a.k_cache, 4, dims, strides, box, a.dtype) ||
       !make_tmap(&mv, a.v_cache, 4, dims, strides, box, a.dtype))
     return cudaErrorInvalidValue;
+  // the queries [total_q][Hq][128] as 64 columns, heads, column halves, tokens; a
+  // box is 128 / G tokens of a kv head's G query heads
+  const int G = a.Hq / a.Hkv;
+  const int64_t qdims[4] = {64, a.Hq, 2, a.total_q};
+  const int64_t qstrides[3] = {DH * 2, 128, static_cast<int64_t>(a.Hq) * DH * 2};
+  const int qbox[4] = {64, G, 1, MR / G};
+  if (!make_tmap(&mq, a.q, 4, qdims, qstrides, qbox, a.dtype)) return cudaErrorInvalidValue;
   Params p;
   p.out = a.out;
   p.q = a.q;
@@ -603,7 +604,7 @@ cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream)
   p.total_q = a.total_q;
   p.Hq = a.Hq;
   p.Hkv = a.Hkv;
-  p.G = a.Hq / a.Hkv;
+  p.G = G;
   p.num_blocks = a.num_blocks;
   p.block_size = a.block_size;
   p.partition_size = a.partition_size;
@@ -614,7 +615,7 @@ cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream)
   const int64_t ctas = static_cast<int64_t>(a.num_seqs) * a.Hkv * p.n_pairs * a.num_partitions;
   if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
   return launch_overlapped(kern, dim3(static_cast<unsigned>(ctas)), dim3(THREADS), SMEM_BYTES,
-                           stream, p, mk, mv);
+                           stream, p, mk, mv, mq);
 }
 
 template <typename T>
