@@ -237,7 +237,7 @@ pa_status copy_scaled(const char* fn, void* dst_k, void* dst_v, float* dst_ks, f
   if (!status) return PA_ERR_CUDA;
   const pa::CopyScaled c = {{dst_k, dst_v},   {src_k, src_v}, {dst_ks, dst_vs}, {src_ks, src_vs},
                             pairs,            num_pairs,      src_blocks,       dst_blocks,
-                            num_kv_heads,     head_size,      block_size};
+                            num_kv_heads,     head_size,      block_size,       src_k == dst_k};
   return launch_status(fn, pa::launch_copy_block_scaled(c, status, stream), 1);
 }
 

@@ -317,7 +317,7 @@ struct CopyParams {
 };
 
 // Block pairs[p][1] of the destination := block pairs[p][0] of the source, codes
-// and scales; blockIdx.z selects K or V, a thread moves four 16-byte chunks
+// and scales, between any memories that the GPU addresses (swap); blockIdx.z selects K or V, a thread moves four 16-byte chunks
 // with all four loads in flight.
 __global__ void __launch_bounds__(256) copy_block_scaled_kernel(const CopyParams p) {
   allow_dependents();
@@ -347,6 +347,137 @@ __global__ void __launch_bounds__(256) copy_block_scaled_kernel(const CopyParams
         p.dst_scales[kv][dst * p.Hkv + h] = p.src_scales[kv][src * p.Hkv + h];
     }
   }
+}
+
+// The same within device memory, through shared memory with bulk copies: a warp
+// keeps kStages pieces of up to 16 KB in flight, each loaded by one instruction
+// and stored by another as soon as it has landed, so that no register or issue
+// slot carries the data.  A second warp copies the scales.
+// Bound by HBM: 8192 blocks of 32 KB (538 MB read and written) in 92 us, 5.8
+// TB/s (107 us with four 16-byte loads and stores per thread).
+constexpr int kPiece = 16384;
+constexpr int kStages = 6;
+
+__device__ __forceinline__ void bulk_store(void* gmem_dst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(gmem_dst),
+               "r"(smem_addr(smem_src)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void bulk_commit() {
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// Until at most N of this thread's latest store groups still read shared memory.
+template <int N>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+
+__global__ void __launch_bounds__(64) copy_block_bulk_kernel(const CopyParams p) {
+  allow_dependents();
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kStages];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 1) {
+    const int64_t n = static_cast<int64_t>(p.num_pairs) * p.Hkv;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * 32 + lane; i < n;
+         i += static_cast<int64_t>(gridDim.x) * 32) {
+      const int64_t pr = i / p.Hkv, h = i - pr * p.Hkv;
+      const int64_t src = __ldg(p.pairs + 2 * pr), dst = __ldg(p.pairs + 2 * pr + 1);
+      if (src < 0 || src >= p.src_blocks || dst < 0 || dst >= p.dst_blocks) {
+        if (h == 0) atomicOr(p.status, PA_DEVERR_PAIR);
+        continue;
+      }
+      const float k = p.src_scales[0][src * p.Hkv + h], v = p.src_scales[1][src * p.Hkv + h];
+      p.dst_scales[0][dst * p.Hkv + h] = k;
+      p.dst_scales[1][dst * p.Hkv + h] = v;
+    }
+    return;
+  }
+  if (lane == 0) {
+    for (int s = 0; s < kStages; ++s) mbar_init(&full[s], 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  // item i of this CTA: piece c of pair pr of cache kv, in that order from slow to fast
+  const int64_t block_bytes = p.chunks * 16;
+  const int pieces = static_cast<int>((block_bytes + kPiece - 1) / kPiece);
+  const int64_t total = static_cast<int64_t>(p.num_pairs) * 2 * pieces;
+  const int64_t mine =
+      total > blockIdx.x ? (total - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  int64_t src_at = 0, dst_at = 0;      // lane l: item 32 g + l of the group last looked up
+  uint32_t bytes_at = 0;               // 0: nothing to copy (a bad pair)
+  const char* from = nullptr;
+  char* to = nullptr;
+  auto look_up = [&](int64_t i) {      // every lane its item of the group that i begins
+    const int64_t item = (i + lane) * gridDim.x + blockIdx.x;
+    bytes_at = 0;
+    if (item >= total) return;
+    const int64_t pr = item / (2 * pieces);
+    const int rest = static_cast<int>(item - pr * 2 * pieces), kv = rest / pieces, c = rest % pieces;
+    const int64_t src = __ldg(p.pairs + 2 * pr), dst = __ldg(p.pairs + 2 * pr + 1);
+    if (src < 0 || src >= p.src_blocks || dst < 0 || dst >= p.dst_blocks) return;
+    src_at = src * block_bytes + static_cast<int64_t>(c) * kPiece;
+    dst_at = dst * block_bytes + static_cast<int64_t>(c) * kPiece;
+    from = reinterpret_cast<const char*>(p.src[kv]);
+    to = reinterpret_cast<char*>(p.dst[kv]);
+    bytes_at = static_cast<uint32_t>(min(block_bytes - static_cast<int64_t>(c) * kPiece,
+                                         static_cast<int64_t>(kPiece)));
+  };
+  // what each stage holds, known to lane 0
+  char* target[kStages];
+  uint32_t size[kStages];
+  auto load = [&](int64_t i, int s) {  // item i into stage s (i ascends over the calls)
+    if ((i & 31) == 0) look_up(i);
+    const int l = static_cast<int>(i & 31);
+    const uint32_t n = __shfl_sync(FULL, bytes_at, l);
+    const char* f = reinterpret_cast<const char*>(
+        __shfl_sync(FULL, reinterpret_cast<unsigned long long>(from + src_at), l));
+    char* t = reinterpret_cast<char*>(
+        __shfl_sync(FULL, reinterpret_cast<unsigned long long>(to + dst_at), l));
+    target[s] = t;
+    size[s] = n;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(&full[s], n);
+      if (n > 0) bulk_load(ring + s * kPiece, f, n, &full[s]);
+    }
+  };
+  bool ok = true;
+  for (int s = 0; s < kStages; ++s)
+    if (s < mine) load(s, s);
+  for (int64_t i0 = 0; i0 < mine && ok; i0 += kStages) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) {
+      const int64_t i = i0 + s;
+      if (i >= mine || !ok) break;
+      if (lane == 0) {
+        ok = mbar_wait(&full[s], static_cast<uint32_t>(i0 / kStages) & 1, p.status);
+        if (ok && size[s] > 0) bulk_store(target[s], ring + s * kPiece, size[s]);
+        bulk_commit();
+      }
+      ok = __all_sync(FULL, ok);
+      // the stage of the item before: its store has read it; refill it
+      if (ok && i >= 1 && i - 1 + kStages < mine) {
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        load(i - 1 + kStages, (s + kStages - 1) % kStages);
+      }
+    }
+  }
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  if (!ok && lane == 0) {   // wait (bounded) for copies still in flight
+    for (int s = 0; s < kStages; ++s) {
+      mbar_wait(&full[s], 0, p.status, 1000000);
+      mbar_wait(&full[s], 1, p.status, 1000000);
+    }
+  }
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
 }
 
 int log2_of(int x) {
@@ -421,6 +552,17 @@ int launch_copy_block_scaled(const CopyScaled& c, unsigned int* status, void* st
   p.chunks = static_cast<int64_t>(c.Hkv) * c.block_size * c.D / 16;
   p.num_pairs = c.num_pairs;
   p.Hkv = c.Hkv;
+  if (c.device) {
+    constexpr int smem = kStages * kPiece;
+    const cudaError_t e =
+        cudaFuncSetAttribute(copy_block_bulk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const int64_t items = static_cast<int64_t>(c.num_pairs) * 2 * ((p.chunks * 16 + kPiece - 1) / kPiece);
+    const int64_t most = 2ll * num_sms();
+    copy_block_bulk_kernel<<<static_cast<unsigned>(items < most ? items : most), 64, smem,
+                             static_cast<cudaStream_t>(stream)>>>(p);
+    return cudaGetLastError();
+  }
   int64_t gx = (p.chunks + 1023) / 1024;
   if (gx > 1024) gx = 1024;
   const int gy = c.num_pairs < 65535 ? c.num_pairs : 65535;
