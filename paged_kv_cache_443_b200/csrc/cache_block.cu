@@ -51,22 +51,33 @@ __device__ __forceinline__ uint32_t codes4(const float* f) {
   return codes2(f[0], f[1]) | (codes2(f[2], f[3]) << 16);
 }
 
-// max |x| of a 16-byte chunk, NaNs aside.  16-bit types: magnitudes compare as
-// bits, two at a time, without widening (which costs the registers of all the
-// widened elements); a NaN's bits are above infinity's.
+// max |x| over 16-byte chunks, NaNs aside, gathered as bits.  16-bit types:
+// magnitudes compare as integers, two at a time, without widening (which would
+// take registers for all the widened elements); a NaN's bits are above
+// infinity's, and bits_max() then says so by NaN.  32-bit: fmax drops NaNs.
 template <typename T>
-__device__ __forceinline__ float chunk_max(const uint4& v) {
-  float m = 0.f;
+__device__ __forceinline__ void gather_max(uint32_t& m, const uint4& v) {
   if constexpr (sizeof(T) == 2) {
-    const uint32_t a = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-    const uint32_t most = max(a & 0xffffu, a >> 16);
-    constexpr bool bf = std::is_same<T, __nv_bfloat16>::value;
-    if (most <= (bf ? 0x7f80u : 0x7c00u))
-      return bf ? __uint_as_float(most << 16)
-                : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+    m = __vmaxu2(m, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+  } else {
+    const float a = fmaxf(fabsf(__uint_as_float(v.x)), fabsf(__uint_as_float(v.y)));
+    const float b = fmaxf(fabsf(__uint_as_float(v.z)), fabsf(__uint_as_float(v.w)));
+    m = __float_as_uint(fmaxf(__uint_as_float(m), fmaxf(a, b)));
   }
-  float f[Elem<T>::EPL];
+}
+template <typename T>
+__device__ __forceinline__ float bits_max(uint32_t m) {
+  if constexpr (sizeof(T) == 4) return __uint_as_float(m);
+  const uint32_t most = max(m & 0xffffu, m >> 16);
+  return std::is_same<T, __nv_bfloat16>::value
+             ? __uint_as_float(most << 16)
+             : __half2float(__ushort_as_half(static_cast<unsigned short>(most)));
+}
+// The same of one chunk where there are NaNs.
+template <typename T>
+__device__ __forceinline__ float plain_max(const uint4& v) {
+  float f[Elem<T>::EPL], m = 0.f;
   Elem<T>::unpack(v, f);
 #pragma unroll
   for (int e = 0; e < Elem<T>::EPL; ++e) m = fmaxf(m, fabsf(f[e]));
@@ -84,17 +95,49 @@ struct AppendParams {
   int positions;           // list positions a warp looks after
 };
 
-// x / now for EPL elements and their codes at dst.  A power of two divides exactly
-// as its reciprocal multiplies.
-template <int EPL>
-__device__ __forceinline__ void store_codes(float* f, float now, uint8_t* dst) {
-  if ((__float_as_uint(now) & 0x7fffffu) == 0) {
-    const float inv = __frcp_rn(now);
+// How the elements are divided by a scale: a power of two divides exactly as its
+// reciprocal multiplies; f16 elements by one that f16 holds as a normal number
+// stay f16 pairs (a product that f16 cannot hold exactly is below 2^-14, far
+// inside the half step below E4M3's smallest code).
+struct Divide {
+  float by, inv;
+  uint32_t inv2;       // the reciprocal as an f16 pair, 0: not that way
+};
+template <typename T>
+__device__ __forceinline__ Divide divide_by(float scale) {
+  Divide d{scale, 0.f, 0u};
+  if ((__float_as_uint(scale) & 0x7fffffu) == 0) {
+    d.inv = __frcp_rn(scale);
+    if (std::is_same<T, __half>::value && scale >= 0.000030517578125f && scale <= 16384.f) {
+      const __half2 h = __float2half2_rn(d.inv);
+      d.inv2 = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  }
+  return d;
+}
+__device__ __forceinline__ uint32_t codes2_h(uint32_t x, uint32_t inv2) {
+  const __half2 p = __hmul2(*reinterpret_cast<const __half2*>(&x), *reinterpret_cast<const __half2*>(&inv2));
+  return static_cast<uint32_t>(
+      __nv_cvt_halfraw2_to_fp8x2(static_cast<__half2_raw>(p), __NV_SATFINITE, __NV_E4M3));
+}
+// The codes of a chunk's elements at dst.
+template <typename T>
+__device__ __forceinline__ void store_codes(const uint4& v, const Divide& d, uint8_t* dst) {
+  constexpr int EPL = Elem<T>::EPL;
+  if (std::is_same<T, __half>::value && d.inv2 != 0) {
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(codes2_h(v.x, d.inv2) | (codes2_h(v.y, d.inv2) << 16),
+                   codes2_h(v.z, d.inv2) | (codes2_h(v.w, d.inv2) << 16));
+    return;
+  }
+  float f[EPL];
+  Elem<T>::unpack(v, f);
+  if (d.inv != 0.f) {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) f[e] *= inv;
+    for (int e = 0; e < EPL; ++e) f[e] *= d.inv;
   } else {
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) f[e] = __fdiv_rn(f[e], now);
+    for (int e = 0; e < EPL; ++e) f[e] = __fdiv_rn(f[e], d.by);
   }
   if constexpr (EPL == 8)
     *reinterpret_cast<uint2*>(dst) = make_uint2(codes4(f), codes4(f + 4));
@@ -202,7 +245,10 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     float most = 0.f;                        // of position `lane`
 #pragma unroll
     for (int k = 0; k < IT; ++k) {
-      float m = chunk_max<T>(v[k]);
+      uint32_t bits = 0;
+      gather_max<T>(bits, v[k]);
+      float m = bits_max<T>(bits);
+      if (isnan(m)) m = plain_max<T>(v[k]);
 #pragma unroll
       for (int o = LPR / 2; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(FULL, m, o));
       m = __shfl_sync(FULL, m, (lane % RPW) * LPR);
@@ -240,9 +286,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
       const int off = __shfl_sync(FULL, offset, r);
       const float by = __shfl_sync(FULL, now, r);
       if (((rows_in >> r) & 1u) == 0) continue;
-      float f[EPL];
-      Elem<T>::unpack(v[k], f);
-      store_codes<EPL>(f, by, cache + (((static_cast<int64_t>(b) * p.Hkv + h) << p.log2_bs) + off) * D + col);
+      store_codes<T>(v[k], divide_by<T>(by), cache + (((static_cast<int64_t>(b) * p.Hkv + h) << p.log2_bs) + off) * D + col);
     }
     leaders &= ~many;
   }
@@ -282,13 +326,22 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     float most = 0.f;
     for (int t0 = 0; t0 < n; t0 += kChunk) {
       load(t0);
+      uint32_t bits = 0;
 #pragma unroll
-      for (int k = 0; k < IT; ++k) most = fmaxf(most, chunk_max<T>(v[k]));
+      for (int k = 0; k < IT; ++k) gather_max<T>(bits, v[k]);
+      float m = bits_max<T>(bits);
+      if (isnan(m)) {
+        m = 0.f;
+#pragma unroll
+        for (int k = 0; k < IT; ++k) m = fmaxf(m, plain_max<T>(v[k]));
+      }
+      most = fmaxf(most, m);
     }
     most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));   // >= 0: ordered as bits
     const float now = fmaxf(old, scale_for(most));
     if (now > old && !fresh) rescale<D>(rows, bs, written, old, now);
     if (lane == 0) scales[row0] = now;
+    const Divide div = divide_by<T>(now);
     for (int t0 = 0; t0 < n; t0 += kChunk) {
       if (n > kChunk) load(t0);
 #pragma unroll
@@ -297,9 +350,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
         int off = __shfl_sync(FULL, offset, (at + t) & 31);
         if (t >= n) continue;
         if (at + t >= 32) off = static_cast<int>(__ldg(p.slots + first + t)) & (bs - 1);
-        float f[EPL];
-        Elem<T>::unpack(v[k], f);
-        store_codes<EPL>(f, now, rows + off * D + col);
+        store_codes<T>(v[k], div, rows + off * D + col);
       }
     }
   }
