@@ -67,10 +67,12 @@ constexpr int QT_BYTES = NPAD * DH;         // one query term: 16 rows x 128 cod
 constexpr int PT_BYTES = NPAD * TOK;        // one P term: 128 tokens x 16 heads (MN-major)
 constexpr int PB_BYTES = PTERM * PT_BYTES;  // one P buffer (both terms)
 constexpr int THREADS = 192;
-constexpr int TMEM_COLS = 64;               // S0 [0,16), S1 [16,32), O [32,48)
+constexpr int TMEM_COLS = 64;               // S0 [0,16), S1 [16,32), O [32,48), BS: O2 [48,64)
 constexpr float RESCALE_THRESHOLD = 2.0f;   // P <= 2^2
 constexpr float P_UP = 64.0f;               // P * 2^6 <= 256 < 448
 constexpr float P_DOWN = 1.0f / 64.0f;
+constexpr float P2_UP = 32.0f;              // BS: a residual of P1 (<= 8) as the second term
+constexpr float P2_DOWN = 1.0f / 32.0f;
 
 // 2^x by the hardware's approximate base-2 exponential (flushes subnormals).
 __device__ __forceinline__ float ex2_fast(float x) {
@@ -197,7 +199,11 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // number to it: the key scale joins the score's factor, the value scale its
 // exponent (P = 2^(s + log2 vs - m) weights the raw codes, and the running max
 // guards the products p vs), and the partial sum adds P / vs.  The thread reads
-// its block's scales a tile ahead and the block's id two.
+// its block's scales a tile ahead and the block's id two.  The second term of P
+// is taken 2^5 times as large, into an accumulator of its own (O2, added as
+// 2^-5 O2 at the end): P is then held to 2^-8 of its value down to 2^-17 (2^-12
+// with both terms in one), so that many small weights beside a large one -- a
+// long context behind an attention sink -- do not sink into E4M3's subnormals.
 template <typename T, int G, typename Y, int NQ = 1, bool BS = false>
 __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     decode_partition_tc8_kernel(const Tc8Params p, const __grid_constant__ CUtensorMap tmap_k,
@@ -488,7 +494,10 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
             const uint64_t a = smem_desc(v_a + s * TILE_BYTES + k * 4096, 1024, 1024);
             const uint64_t bp =
                 smem_desc_plain(p_a + (i % PBUF) * PB_BYTES + term * PT_BYTES + k * 32 * NPAD, 128, 128);
-            mma_e4m3(d, a, bp, kIdescE4M3_AMN_BMN, (!first || term > 0 || k > 0) ? 1u : 0u);
+            if (BS)
+              mma_e4m3(d + term * NPAD, a, bp, kIdescE4M3_AMN_BMN, (!first || k > 0) ? 1u : 0u);
+            else
+              mma_e4m3(d, a, bp, kIdescE4M3_AMN_BMN, (!first || term > 0 || k > 0) ? 1u : 0u);
           }
         }
         mma_commit(&vr_empty[s]);
@@ -507,12 +516,14 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     const int quad = warp & 3;
     const int r = quad * 32 + lane;
     const uint32_t lane_base = static_cast<uint32_t>(quad * 32) << 16;
-    float m_run[NC], l_part[NC], sc[NC];
+    // BS reads the columns' factors from shared memory every tile, a float4 at a
+    // time: in registers they would be the ones that spill
+    float m_run[NC], l_part[NC], sc[BS ? 1 : NC];
 #pragma unroll
     for (int h = 0; h < NC; ++h) {
       m_run[h] = -INFINITY;
       l_part[h] = 0.f;
-      sc[h] = p.scale_log2 * qs[h];
+      if (!BS) sc[BS ? 0 : h] = p.scale_log2 * qs[h];
     }
     int pb_next = -1;
     float ks_next = 1.f, vs_next = 1.f;
@@ -542,6 +553,12 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       tc_fence_after();
       float o[16];
       tmem_ld16(tmem + lane_base + 2 * NPAD, o);
+      if constexpr (BS) {
+        float o2[16];
+        tmem_ld16(tmem + lane_base + 3 * NPAD, o2);
+#pragma unroll
+        for (int h = 0; h < NC; ++h) o[h] = fmaf(o2[h], P2_DOWN, o[h]);
+      }
       tc_fence_before();
       __syncwarp();
 #pragma unroll
@@ -591,7 +608,7 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       float ks = 1.f, lvs = 0.f, rvs = 1.f;
       if constexpr (BS) {
         const float vs = fminf(fmaxf(vs_next, kScaleMin), kScaleMax);
-        ks = fminf(fmaxf(ks_next, kScaleMin), kScaleMax);
+        ks = fminf(fmaxf(ks_next, kScaleMin), kScaleMax) * p.scale_log2;
         lvs = __log2f(vs);
         rvs = __frcp_rn(vs);
         scales_of(pb_next);
@@ -612,7 +629,10 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       bool need = false;
 #pragma unroll
       for (int h = 0; h < NC; ++h) {
-        s[h] = valid && h / G < Qb ? (BS ? fmaf(sv[h] * sc[h], ks, lvs) : sv[h] * sc[h]) : -INFINITY;
+        if constexpr (BS)
+          s[h] = valid ? fmaf(sv[h] * qs[h], ks, lvs) : -INFINITY;
+        else
+          s[h] = valid && h / G < Qb ? sv[h] * sc[h] : -INFINITY;
         need |= s[h] > m_run[h] + RESCALE_THRESHOLD;
       }
       if (bar_or(1, 128, need)) {
@@ -642,6 +662,12 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
 #pragma unroll
           for (int h = 0; h < NC; ++h) o[h] *= alpha[h];
           tmem_st16(tmem + lane_base + 2 * NPAD, o);
+          if constexpr (BS) {
+            tmem_ld16(tmem + lane_base + 3 * NPAD, o);
+#pragma unroll
+            for (int h = 0; h < NC; ++h) o[h] *= alpha[h];
+            tmem_st16(tmem + lane_base + 3 * NPAD, o);
+          }
         }
       }
       float pr[NC];
@@ -661,7 +687,12 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
         const float x1 = (h + 1 < NC) ? pr[h + 1] * P_UP : 0.f;
         const uint32_t c1 = to_e4m3x2(x0, x1);
         const float2 d1 = from_e4m3x2(c1);
-        const uint32_t c2 = to_e4m3x2(x0 - d1.x, x1 - d1.y);
+        uint32_t c2;
+        if constexpr (BS)   // (x - d1) * P2_UP, exactly
+          c2 = to_e4m3x2(fmaf(-P2_UP, d1.x, pr[h] * (P_UP * P2_UP)),
+                         fmaf(-P2_UP, d1.y, (h + 1 < NC ? pr[h + 1] : 0.f) * (P_UP * P2_UP)));
+        else
+          c2 = to_e4m3x2(x0 - d1.x, x1 - d1.y);
         w1[h >> 2] |= c1 << ((h & 2) * 8);
         w2[h >> 2] |= c2 << ((h & 2) * 8);
       }

@@ -303,9 +303,10 @@ def test_decode_scales_far_apart(dtype, group):
 
 @pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
 @pytest.mark.parametrize("group", [2, 4, 8])
-def test_decode_one_key_over_many(dtype, group):
-    """A key that outweighs each of 6000 others by e^7, which together outweigh it:
-    small weights must not be lost, whatever the blocks' scales."""
+@pytest.mark.parametrize("over", [7.0, 9.7])
+def test_decode_one_key_over_many(dtype, group, over):
+    """A key that outweighs each of 6000 others by e^7 (e^9.7 = 2^14), which together
+    weigh as much: small weights must not be lost, whatever the blocks' scales."""
     gen = torch.Generator().manual_seed(group)
     batch = Batch(gen, [6001], 1, 16, 128, v_range=(-7, -6))
     q = torch.sign(torch.randn(1, group, 128, generator=gen))
@@ -315,7 +316,7 @@ def test_decode_one_key_over_many(dtype, group):
     batch.k[batch.table[0, 0].long(), 0, 0] = torch.from_numpy(one)
     batch.ks[:] = 1.0
     batch.v[batch.table[0, :376].long()] &= 0x7f      # positive values: no cancellation
-    scale = 7.0 / (64 * 128)
+    scale = over / (64 * 128)
     got = batch.check(q.to(dtype), scale)
     out, _ = batch.want(q.to(dtype), scale)
     # far inside the worst case: the mean of the weights' rounding errors
