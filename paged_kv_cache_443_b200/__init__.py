@@ -202,14 +202,18 @@ def _contig(*ts):
             raise PagedKVError(PA_ERR_INVALID, "tensors must be contiguous")
 
 
-def _current_device(*ts):
-    """Refuses device tensors that are not on the current CUDA device (kernels run
-    there, on its current stream unless one is given)."""
+def _ready(*ts):
+    """Refuses tensors that are not contiguous or not on the current CUDA device
+    (kernels run there, on its current stream unless one is given)."""
     dev = _t().cuda.current_device() if ts[0].is_cuda else -2
     for t in ts:
-        if t is not None and t.get_device() != dev:
+        if t is None:
+            continue
+        if t.get_device() != dev:
             raise PagedKVError(PA_ERR_INVALID,
                                f"tensors must be on the current CUDA device (got {t.device})")
+        if not t.is_contiguous():
+            raise PagedKVError(PA_ERR_INVALID, "tensors must be contiguous")
 
 
 # ---------------------------------------------------------------------------
@@ -275,8 +279,9 @@ def pa_decode_workspace_bytes(num_seqs: int, num_heads: int, head_size: int,
 
 
 def _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
-                 max_context_len, workspace, stream, kv_dtype=None):
-    _contig(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+                 max_context_len, workspace, stream, kv_dtype=None, ready=False):
+    if not ready:
+        _contig(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
     B, Hq, D = shape = q.shape
     NB, Hkv, bs, D2 = pool = k_cache.shape
     if D2 != D or out.shape != shape or v_cache.shape != pool:
@@ -435,7 +440,6 @@ def _scales(cache, *scales):
     for t in scales:
         if t.dtype != f32 or t.shape != shape:
             raise PagedKVError(PA_ERR_INVALID, "scales must be float32 [num_blocks, Hkv]")
-    _contig(*scales)
 
 
 def pa_decode_fp8_block(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
@@ -444,15 +448,13 @@ def pa_decode_fp8_block(out, q, k_cache, v_cache, k_scales, v_scales, block_tabl
     """pa_decode over E4M3 caches with a scale per (block, kv head): codes of
     block i and kv head h stand for code * k_scales[i, h] (v_scales for values);
     q and out f32 / f16 / bf16."""
-    torch = _t()
-    _current_device(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
-                    workspace)
+    _ready(q, out, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
-                     max_context_len, workspace, stream, kv_dtype=torch.float8_e4m3fn)
+                     max_context_len, workspace, stream, _t().float8_e4m3fn, True)
     _scales(k_cache, k_scales, v_scales)
-    if context_lens.numel() != a[7] or block_tables.shape[0] != a[7]:
+    if len(context_lens) != a[7] or len(block_tables) != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
-    _check(lib().pa_decode_fp8_block(*a[:4], _ptr(k_scales), _ptr(v_scales), *a[4:]))
+    _check(lib().pa_decode_fp8_block(*a[:4], k_scales.data_ptr(), v_scales.data_ptr(), *a[4:]))
 
 
 def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping,
@@ -462,37 +464,37 @@ def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_sca
     element, never below the stored one (a block whose first slot is written
     starts anew); the block's older codes follow when it grows.  The tokens of a
     block stand next to each other in slot_mapping."""
-    _contig(key, value, k_cache, v_cache, slot_mapping)
+    _ready(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
     torch = _t()
-    N, Hkv, D = key.shape
-    NB, Hkv2, bs, D2 = k_cache.shape
-    if (Hkv2, D2) != (Hkv, D) or value.shape != key.shape or v_cache.shape != k_cache.shape:
+    N, Hkv, D = shape = key.shape
+    NB, Hkv2, bs, D2 = pool = k_cache.shape
+    if Hkv2 != Hkv or D2 != D or value.shape != shape or v_cache.shape != pool:
         raise PagedKVError(PA_ERR_INVALID, "shape mismatch")
     if slot_mapping.dtype != torch.int64 or slot_mapping.numel() != N:
         raise PagedKVError(PA_ERR_INVALID, "slot_mapping must be int64 [N]")
     if key.dtype != value.dtype or not (k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn):
         raise PagedKVError(PA_ERR_INVALID, "key/value share a dtype; caches are float8_e4m3fn")
     _scales(k_cache, k_scales, v_scales)
-    _current_device(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
     _check(lib().pa_reshape_and_cache_fp8_block(
-        _ptr(key), _ptr(value), _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-        _ptr(slot_mapping), N, Hkv, D, bs, NB, _dtype_code(key), _stream(stream)))
+        key.data_ptr(), value.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        k_scales.data_ptr(), v_scales.data_ptr(), slot_mapping.data_ptr(), N, Hkv, D, bs, NB,
+        _dtype_code(key), _stream(stream)))
 
 
 def _scaled_pool(k_cache, v_cache, k_scales, v_scales):
-    torch = _t()
-    _contig(k_cache, v_cache)
+    f8 = _t().float8_e4m3fn
     if v_cache.shape != k_cache.shape:
         raise PagedKVError(PA_ERR_INVALID, "cache shape mismatch")
-    if not (k_cache.dtype == v_cache.dtype == torch.float8_e4m3fn):
+    if not (k_cache.dtype == v_cache.dtype == f8):
         raise PagedKVError(PA_ERR_INVALID, "the caches must be float8_e4m3fn")
     _scales(k_cache, k_scales, v_scales)
-    if k_cache.device.type != "cuda":   # a pool in host memory is read by the GPU
-        for t in (k_cache, v_cache, k_scales, v_scales):
-            if t.device.type != "cpu" or not t.is_pinned():
-                raise PagedKVError(PA_ERR_INVALID, "a host pool must be pinned memory")
-    else:
-        _current_device(k_cache, v_cache, k_scales, v_scales)
+    if k_cache.is_cuda:
+        _ready(k_cache, v_cache, k_scales, v_scales)
+        return
+    _contig(k_cache, v_cache, k_scales, v_scales)
+    for t in (k_cache, v_cache, k_scales, v_scales):   # host memory that the GPU reads
+        if t.device.type != "cpu" or not t.is_pinned():
+            raise PagedKVError(PA_ERR_INVALID, "a host pool must be pinned memory")
 
 
 def _pairs(block_pairs):
@@ -609,10 +611,10 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale
                      max_context_len, rule: ScoreRule, partition_size=0, workspace=None,
                      stream=None) -> None:
     """pa_decode under a score rule (capped, distance-biased, windowed scores)."""
-    _current_device(out, q, k_cache, v_cache, block_tables, context_lens, workspace)
+    _ready(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
-                     max_context_len, workspace, stream)
-    if context_lens.numel() != a[7] or block_tables.shape[0] != a[7]:
+                     max_context_len, workspace, stream, None, True)
+    if len(context_lens) != a[7] or len(block_tables) != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
     r = rule._struct(q, a[7])
     _check(lib().pa_decode_scored(*a[:15], ctypes.byref(r), *a[15:]))
@@ -624,8 +626,7 @@ def pa_decode_multi_scored(out, q, k_cache, v_cache, block_tables, context_lens,
                            stream=None) -> None:
     """pa_decode_multi under a score rule, with document starts per query token
     and prefixes attended in both directions."""
-    _current_device(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc,
-                    workspace)
+    _ready(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace)
     a = _multi_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
                     max_context_len, max_query_len, partition_size, workspace, stream)
     if block_tables.shape[0] != context_lens.shape[0]:
