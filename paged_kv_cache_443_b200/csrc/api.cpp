@@ -46,10 +46,7 @@ int num_sms() {
 // CTA) the longest of 4096 / 2048 / 1024 tokens; for the CUDA-core kernel 1024
 // (2048 measured slower at opt13b: fewer, longer CTAs leave the last wave
 // thin); else the default.
-int auto_partition(int num_seqs, int num_heads, int num_kv_heads, int head_size, pa_dtype dtype,
-                   int max_context_len) {
-  const int G = num_kv_heads > 0 ? num_heads / num_kv_heads : 0;
-  const bool tc = (dtype == PA_F16 || dtype == PA_BF16) && head_size == 128 && (G == 4 || G == 8);
+int auto_partition(bool tc, int num_seqs, int num_kv_heads, int max_context_len) {
   const int64_t want = 8ll * num_sms();
   for (int P : {4096, 2048, 1024}) {
     if (!tc && P > 1024) continue;
@@ -57,6 +54,13 @@ int auto_partition(int num_seqs, int num_heads, int num_kv_heads, int head_size,
     if (ctas >= want) return P;
   }
   return pa::kDefaultPartition;
+}
+
+int auto_partition(int num_seqs, int num_heads, int num_kv_heads, int head_size, pa_dtype dtype,
+                   int max_context_len) {
+  const int G = num_kv_heads > 0 ? num_heads / num_kv_heads : 0;
+  const bool tc = (dtype == PA_F16 || dtype == PA_BF16) && head_size == 128 && (G == 4 || G == 8);
+  return auto_partition(tc, num_seqs, num_kv_heads, max_context_len);
 }
 
 size_t workspace_bytes(int64_t B, int64_t Hq, int64_t D, int64_t NP) {
@@ -152,6 +156,7 @@ pa_status check_decode_full(const char* fn, void* out, const void* q, const void
   a->num_blocks = num_blocks;
   a->partition_size = P;
   a->num_partitions = static_cast<int>(NP);
+  a->max_context_len = max_context_len;
   a->scale = scale;
   a->dtype = dtype;
   a->kv_dtype = dtype;
@@ -829,8 +834,10 @@ extern "C" pa_status pa_decode_fp8_block(void* out, const void* q, const void* k
                                          size_t workspace_bytes_in, void* stream) {
   const char* fn = "pa_decode_fp8_block";
   if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
-    partition_size =
-        auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, max_context_len);
+    partition_size = auto_partition(
+        head_size == 128 &&
+            pa::decode_block_on_tc(dtype, num_heads / num_kv_heads, max_context_len),
+        num_seqs, num_kv_heads, max_context_len);
   pa::DecodeArgs a;
   pa_status st = check_decode_fp8(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                   context_lens, num_seqs, num_heads, num_kv_heads, head_size,

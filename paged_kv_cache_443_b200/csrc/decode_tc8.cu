@@ -61,17 +61,14 @@ constexpr unsigned FULL = 0xffffffffu;
 constexpr int TOK = 128;                    // tokens per tile
 constexpr int NPAD = 16;                    // MMA N (heads padded)
 constexpr int DH = 128;                     // head size
-constexpr int PTERM = 2;                    // E4M3 terms of P
 constexpr int TILE_BYTES = TOK * DH;        // one tile of codes: 16 KB
 constexpr int QT_BYTES = NPAD * DH;         // one query term: 16 rows x 128 codes
 constexpr int PT_BYTES = NPAD * TOK;        // one P term: 128 tokens x 16 heads (MN-major)
-constexpr int PB_BYTES = PTERM * PT_BYTES;  // one P buffer (both terms)
 constexpr int THREADS = 192;
-constexpr int TMEM_COLS = 64;               // S0 [0,16), S1 [16,32), O [32,48), BS: O2 [48,64)
 constexpr float RESCALE_THRESHOLD = 2.0f;   // P <= 2^2
 constexpr float P_UP = 64.0f;               // P * 2^6 <= 256 < 448
 constexpr float P_DOWN = 1.0f / 64.0f;
-constexpr float P2_UP = 32.0f;              // BS: a residual of P1 (<= 8) as the second term
+constexpr float P2_UP = 32.0f;              // BS: what a term leaves (<= 8) as the next one
 constexpr float P2_DOWN = 1.0f / 32.0f;
 
 // 2^x by the hardware's approximate base-2 exponential (flushes subnormals).
@@ -88,19 +85,31 @@ __device__ __forceinline__ float ex2_fast(float x) {
 //   2 terms, 2 + 2 slots, 1 P buffer (~73 KB): three CTAs per SM, for bf16
 //     queries (8 significant bits: two 4-bit terms are exact).  A third CTA's
 //     pipeline hides more of each tile's serial chain than a third slot does.
-template <int NTERM_, int SLOTS_, int PBUF_>
+// PACK: for at most 8 columns in use.  A query term then takes 1 KB, its rows 8 -
+// 15 being the next term's (and after the last one the small buffers): they feed
+// only columns that nobody reads.  With it three query terms, rings of two tiles
+// and a P buffer of three terms take exactly a third of the SM's shared memory.
+// PTERM terms of P; TMEM: S0 [0,16), S1 [16,32), O [32,48) and, with block scales,
+// an accumulator for each further term behind it.
+template <int NTERM_, int SLOTS_, int PBUF_, int PTERM_ = 2, bool PACK_ = false>
 struct Lay8 {
-  static constexpr int NTERM = NTERM_, SLOTS = SLOTS_, PBUF = PBUF_;
+  static constexpr int NTERM = NTERM_, SLOTS = SLOTS_, PBUF = PBUF_, PTERM = PTERM_;
+  static constexpr bool PACK = PACK_;
+  static constexpr int QT_STEP = PACK ? 8 * DH : QT_BYTES;
+  static constexpr int PB_BYTES = PTERM * PT_BYTES;   // one P buffer
+  static constexpr int TMEM_COLS = (2 + PTERM) * NPAD <= 64 ? 64 : 128;
   static constexpr int OFF_KR = 0;
   static constexpr int OFF_VR = OFF_KR + SLOTS * TILE_BYTES;
   static constexpr int OFF_Q = OFF_VR + SLOTS * TILE_BYTES;
-  static constexpr int OFF_P = OFF_Q + NTERM * QT_BYTES;
-  static constexpr int OFF_BAR = OFF_P + PBUF * PB_BYTES;
+  static constexpr int OFF_P = OFF_Q + NTERM * QT_STEP + (PACK ? QT_BYTES - QT_STEP : 0);
+  static constexpr int OFF_END = OFF_P + PBUF * PB_BYTES;
+  static constexpr int OFF_BAR = PACK ? OFF_Q + NTERM * QT_STEP : OFF_END;
   static constexpr int NBARS = 4 * SLOTS + 4 + 2 * PBUF + 1;
   static constexpr int OFF_TMEM = (OFF_BAR + NBARS * 8 + 15) / 16 * 16;
   static constexpr int OFF_RED = OFF_TMEM + 16;      // 4 warps x 16 floats
   static constexpr int OFF_QS = OFF_RED + 4 * NPAD * 4;
-  static constexpr int SMEM_USED = OFF_QS + NPAD * 4;
+  static constexpr int SMEM_USED = PACK ? OFF_END : OFF_QS + NPAD * 4;
+  static_assert(!PACK || OFF_QS + NPAD * 4 <= OFF_P, "small buffers in 8 rows");
   static constexpr int SMEM_BYTES = SMEM_USED + 1024;
   static constexpr int CTAS_PER_SM = (228 * 1024) / (SMEM_BYTES + 1024);
   static_assert(OFF_VR % 1024 == 0 && OFF_Q % 1024 == 0 && OFF_P % 1024 == 0 &&
@@ -109,9 +118,14 @@ struct Lay8 {
 };
 using LayF16 = Lay8<3, 3, 2>;
 using LayBF16 = Lay8<2, 2, 1>;
+// Block scales, three CTAs per SM: P in as many terms as the queries' type has
+// bits for (2^-8 of its value in two, 2^-12 in three).
+using LayBlockF16 = Lay8<3, 2, 1, 3, true>;
+using LayBlockBF16 = Lay8<2, 2, 1, 2, true>;
+static_assert(LayBlockF16::CTAS_PER_SM >= 3, "three CTAs per SM");
 static_assert(LayF16::CTAS_PER_SM >= 2, "two CTAs per SM");
 static_assert(LayBF16::CTAS_PER_SM >= 3, "three CTAs per SM");
-static_assert(3 * TMEM_COLS <= 512, "TMEM of three CTAs");
+static_assert(3 * LayBlockF16::TMEM_COLS <= 512, "TMEM of three CTAs");
 
 // Instruction descriptor of kind::f8f6f4: E4M3 x E4M3 (format 0 for both),
 // fp32 accumulation, M = 128, N = 16; A K-major (S) or MN-major (O), B K-major.
@@ -199,16 +213,20 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // number to it: the key scale joins the score's factor, the value scale its
 // exponent (P = 2^(s + log2 vs - m) weights the raw codes, and the running max
 // guards the products p vs), and the partial sum adds P / vs.  The thread reads
-// its block's scales a tile ahead and the block's id two.  The second term of P
-// is taken 2^5 times as large, into an accumulator of its own (O2, added as
-// 2^-5 O2 at the end): P is then held to 2^-8 of its value down to 2^-17 (2^-12
-// with both terms in one), so that many small weights beside a large one -- a
-// long context behind an attention sink -- do not sink into E4M3's subnormals.
+// its block's scales a tile ahead and the block's id two.  What a term of P
+// leaves is the next one 2^5 times as large, into an accumulator of its own (2^-5
+// of it is added at the end): two terms then hold P to 2^-8 of its value down
+// to 2^-17 (2^-12 with both in one accumulator), so that many small weights
+// beside a large one -- a long context behind an attention sink -- do not sink
+// into E4M3's subnormals; f16 queries take a third, 2^-12.
 template <typename T, int G, typename Y, int NQ = 1, bool BS = false>
 __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     decode_partition_tc8_kernel(const Tc8Params p, const __grid_constant__ CUtensorMap tmap_k,
                                 const __grid_constant__ CUtensorMap tmap_v) {
-  constexpr int NTERM = Y::NTERM, SLOTS = Y::SLOTS, PBUF = Y::PBUF;
+  constexpr int NTERM = Y::NTERM, SLOTS = Y::SLOTS, PBUF = Y::PBUF, PTERM = Y::PTERM;
+  constexpr int PB_BYTES = Y::PB_BYTES, TMEM_COLS = Y::TMEM_COLS;
+  static_assert(BS || PTERM == 2, "further accumulators are block scales'");
+  static_assert(!Y::PACK || G * NQ <= 8, "columns in use");
   constexpr int OFF_KR = Y::OFF_KR, OFF_VR = Y::OFF_VR, OFF_Q = Y::OFF_Q, OFF_P = Y::OFF_P;
   constexpr int OFF_BAR = Y::OFF_BAR, OFF_TMEM = Y::OFF_TMEM, OFF_RED = Y::OFF_RED;
   constexpr int OFF_QS = Y::OFF_QS;
@@ -445,7 +463,8 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
         f[4 * k + 3] -= v23.y;
         w[k] = c01 | (c23 << 16);
       }
-      *reinterpret_cast<uint4*>(qop + term * QT_BYTES + row_off) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (!Y::PACK || h < 8)
+        *reinterpret_cast<uint4*>(qop + term * Y::QT_STEP + row_off) = make_uint4(w[0], w[1], w[2], w[3]);
     }
     for (int i = t; i < PBUF * PB_BYTES / 16; i += 128)
       reinterpret_cast<uint4*>(pop)[i] = make_uint4(0, 0, 0, 0);
@@ -472,7 +491,7 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
 #pragma unroll
           for (int k = 0; k < DH / 32; ++k) {   // 32 codes (32 bytes) per MMA
             const uint64_t a = smem_desc(k_a + s * TILE_BYTES + k * 32, 16, 1024);
-            const uint64_t bq = smem_desc(q_a + term * QT_BYTES + k * 32, 16, 1024);
+            const uint64_t bq = smem_desc(q_a + term * Y::QT_STEP + k * 32, 16, 1024);
             mma_e4m3(d, a, bq, kIdescE4M3, (term > 0 || k > 0) ? 1u : 0u);
           }
         }
@@ -554,10 +573,15 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       float o[16];
       tmem_ld16(tmem + lane_base + 2 * NPAD, o);
       if constexpr (BS) {
-        float o2[16];
-        tmem_ld16(tmem + lane_base + 3 * NPAD, o2);
+        float by = P2_DOWN;
 #pragma unroll
-        for (int h = 0; h < NC; ++h) o[h] = fmaf(o2[h], P2_DOWN, o[h]);
+        for (int term = 1; term < PTERM; ++term) {
+          float o2[16];
+          tmem_ld16(tmem + lane_base + (2 + term) * NPAD, o2);
+#pragma unroll
+          for (int h = 0; h < NC; ++h) o[h] = fmaf(o2[h], by, o[h]);
+          by *= P2_DOWN;
+        }
       }
       tc_fence_before();
       __syncwarp();
@@ -663,10 +687,13 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
           for (int h = 0; h < NC; ++h) o[h] *= alpha[h];
           tmem_st16(tmem + lane_base + 2 * NPAD, o);
           if constexpr (BS) {
-            tmem_ld16(tmem + lane_base + 3 * NPAD, o);
 #pragma unroll
-            for (int h = 0; h < NC; ++h) o[h] *= alpha[h];
-            tmem_st16(tmem + lane_base + 3 * NPAD, o);
+            for (int term = 1; term < PTERM; ++term) {
+              tmem_ld16(tmem + lane_base + (2 + term) * NPAD, o);
+#pragma unroll
+              for (int h = 0; h < NC; ++h) o[h] *= alpha[h];
+              tmem_st16(tmem + lane_base + (2 + term) * NPAD, o);
+            }
           }
         }
       }
@@ -681,6 +708,7 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
       // token r's 16 head codes of each term are one 16-byte row of the
       // MN-major P^T operand (columns >= NC are 0)
       uint32_t w1[4] = {0u, 0u, 0u, 0u}, w2[4] = {0u, 0u, 0u, 0u};
+      uint32_t w3[4] = {0u, 0u, 0u, 0u};         // PTERM = 3
 #pragma unroll
       for (int h = 0; h < NC; h += 2) {
         const float x0 = pr[h] * P_UP;
@@ -688,17 +716,25 @@ __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
         const uint32_t c1 = to_e4m3x2(x0, x1);
         const float2 d1 = from_e4m3x2(c1);
         uint32_t c2;
-        if constexpr (BS)   // (x - d1) * P2_UP, exactly
-          c2 = to_e4m3x2(fmaf(-P2_UP, d1.x, pr[h] * (P_UP * P2_UP)),
-                         fmaf(-P2_UP, d1.y, (h + 1 < NC ? pr[h + 1] : 0.f) * (P_UP * P2_UP)));
-        else
+        if constexpr (BS) {   // (x - d1) * P2_UP, exactly, and on
+          const float y0 = fmaf(-P2_UP, d1.x, pr[h] * (P_UP * P2_UP));
+          const float y1 = fmaf(-P2_UP, d1.y, (h + 1 < NC ? pr[h + 1] : 0.f) * (P_UP * P2_UP));
+          c2 = to_e4m3x2(y0, y1);
+          if constexpr (PTERM == 3) {
+            const float2 d2 = from_e4m3x2(c2);
+            w3[h >> 2] |= to_e4m3x2((y0 - d2.x) * P2_UP, (y1 - d2.y) * P2_UP) << ((h & 2) * 8);
+          }
+        } else {
           c2 = to_e4m3x2(x0 - d1.x, x1 - d1.y);
+        }
         w1[h >> 2] |= c1 << ((h & 2) * 8);
         w2[h >> 2] |= c2 << ((h & 2) * 8);
       }
       uint8_t* pb = pop + (i % PBUF) * PB_BYTES + r * NPAD;
       *reinterpret_cast<uint4*>(pb) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
       *reinterpret_cast<uint4*>(pb + PT_BYTES) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+      if constexpr (PTERM == 3)
+        *reinterpret_cast<uint4*>(pb + 2 * PT_BYTES) = make_uint4(w3[0], w3[1], w3[2], w3[3]);
       if (n_valid < TOK) {
         // the last tile: zero the V rows of tokens past the end, so that
         // whatever they hold (unused slots, stale data) adds 0 * 0 to O
@@ -767,7 +803,10 @@ int tc8_parts_per_cta(int64_t rows, int partition_size, int n_parts, int64_t oth
 // slots [0, a.slot_base) of every member's row.
 template <typename T, int G, int NQ, bool BS = false>
 cudaError_t launch_tc8_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
-  using Y = typename std::conditional<std::is_same<T, __nv_bfloat16>::value, LayBF16, LayF16>::type;
+  using Y = typename std::conditional<
+      std::is_same<T, __nv_bfloat16>::value,
+      typename std::conditional<BS, LayBlockBF16, LayBF16>::type,
+      typename std::conditional<BS, LayBlockF16, LayF16>::type>::type;
   constexpr int SMEM_BYTES = Y::SMEM_BYTES;
   constexpr bool grouped = NQ > 1;
   const int q_groups = grouped ? (a.max_group_size + NQ - 1) / NQ : 1;
@@ -823,24 +862,45 @@ cudaError_t launch_tc8_t(const DecodeArgs& a, unsigned int* status, cudaStream_t
 
 }  // namespace
 
+// Over block scales the tensor cores also serve one and two query heads per kv
+// head: the CUDA-core kernel widens every code for every head.  64 sequences of
+// 100-2048 tokens, 0.71 GB: bf16 at one head 176 us there and 116 here, two heads
+// 285 / 117 (bf16) and 180 / 126 (f16).  f16 at one head has the mixed-precision
+// FMA on code pairs there and three terms of q and P here: 128-142 / 124-132,
+// 197 / 175 at 1000-2048 tokens, but 83 / 87 at 300-1000 and 114 / 155 at 20-400.
+bool decode_block_on_tc(pa_dtype dtype, int G, int max_context_len) {
+  return dtype == PA_BF16 || (dtype == PA_F16 && (G >= 2 || max_context_len > 1024));
+}
+
 bool decode_tc8_supported(const DecodeArgs& a) {
   const int G = a.Hq / a.Hkv;
   return a.kv_dtype == PA_FP8_E4M3 && (a.dtype == PA_F16 || a.dtype == PA_BF16) && a.D == DH &&
-         (G == 4 || G == 8) && a.partition_size % TOK == 0 &&
+         (G == 4 || G == 8 ||
+          (a.k_scales != nullptr && decode_block_on_tc(a.dtype, G, a.max_context_len))) &&
+         a.partition_size % TOK == 0 &&
          static_cast<int64_t>(a.num_blocks) * a.Hkv * a.block_size < (int64_t(1) << 31) &&
          tmap_available();
 }
 
+namespace {
+template <typename T>
+int launch_block_scales(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
+  switch (a.Hq / a.Hkv) {
+    case 1:
+      return launch_tc8_t<T, 1, 1, true>(a, status, stream);
+    case 2: return launch_tc8_t<T, 2, 1, true>(a, status, stream);
+    case 4: return launch_tc8_t<T, 4, 1, true>(a, status, stream);
+    default: return launch_tc8_t<T, 8, 1, true>(a, status, stream);
+  }
+}
+}  // namespace
+
 int launch_decode_partitions_tc8(const DecodeArgs& a, unsigned int* status, void* stream) {
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const int G = a.Hq / a.Hkv;
-  if (a.k_scales != nullptr) {
-    if (a.dtype == PA_BF16)
-      return G == 8 ? launch_tc8_t<__nv_bfloat16, 8, 1, true>(a, status, st)
-                    : launch_tc8_t<__nv_bfloat16, 4, 1, true>(a, status, st);
-    return G == 8 ? launch_tc8_t<__half, 8, 1, true>(a, status, st)
-                  : launch_tc8_t<__half, 4, 1, true>(a, status, st);
-  }
+  if (a.k_scales != nullptr)
+    return a.dtype == PA_BF16 ? launch_block_scales<__nv_bfloat16>(a, status, st)
+                              : launch_block_scales<__half>(a, status, st);
   if (a.dtype == PA_BF16) {
     return G == 8 ? launch_tc8_t<__nv_bfloat16, 8, 1>(a, status, st)
                   : launch_tc8_t<__nv_bfloat16, 4, 1>(a, status, st);

@@ -54,6 +54,7 @@ struct DecodeArgs {
   int64_t max_blocks;
   int num_seqs, Hq, Hkv, D, block_size, num_blocks;
   int partition_size, num_partitions;
+  int max_context_len = 0;
   float scale;
   pa_dtype dtype;      // q and out (and the caches unless kv_dtype says otherwise)
   pa_dtype kv_dtype;   // the caches: dtype, or PA_FP8_E4M3
@@ -115,6 +116,7 @@ int launch_decode_group_tc(const DecodeArgs& a, unsigned int* status, void* stre
 // queries, head size 128, 4 or 8 query heads per kv head, partition length a
 // multiple of 128.
 bool decode_tc8_supported(const DecodeArgs& a);  // needs tmap_available()
+bool decode_block_on_tc(pa_dtype dtype, int G, int max_context_len);  // over block scales, head size 128
 int launch_decode_partitions_tc8(const DecodeArgs& a, unsigned int* status, void* stream);
 // The groups' shared spans over an E4M3 cache (pa_decode_grouped_fp8), G = 1, 2, 4, 8.
 bool decode_group_tc8_supported(const DecodeArgs& a);  // needs tmap_available()
