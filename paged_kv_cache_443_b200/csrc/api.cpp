@@ -613,20 +613,24 @@ int even_partition(int P, int span) {
 // so splitting pays only while it fills idle SMs.  Takes the even split with
 // the fewest (tiles + 4) * rounds of CTAs; the reduce counts as one more tile
 // (64 sequences of 4 tokens, window 1024: three partitions 114 us, two 97, one
-// 66).  Never shorter than the default where the workspace was sized by it.
-int auto_partition_few(int64_t ctas_per_part, int span) {
+// 66).  Never more partitions than the default length makes of the whole
+// context, which the workspace was sized by.
+int auto_partition_few(int64_t ctas_per_part, int span, int max_context_len) {
   const int64_t slots = 2ll * num_sms();
-  int best = span < pa::kDefaultPartition ? pa::kDefaultPartition : (span + 127) / 128 * 128;
+  const int whole = span < 128 ? 128 : (span + 127) / 128 * 128;
+  int best = whole;
   int64_t best_cost = -1;
-  for (int np = 1; np <= (span + pa::kDefaultPartition - 1) / pa::kDefaultPartition; ++np) {
-    const int P = np == 1 ? best : even_partition((span + np - 1) / np, span);
-    if (P < pa::kDefaultPartition) break;
+  for (int want = 1; want <= num_partitions(max_context_len, pa::kDefaultPartition); ++want) {
+    const int P = ((span + want - 1) / want + 127) / 128 * 128;
+    if (P < 128) break;
+    const int64_t np = num_partitions(span, P);
     const int64_t rounds = (ctas_per_part * np + slots - 1) / slots;
-    const int64_t cost = rounds * ((P + 127) / 128 + 4) + (np > 1 ? 1 : 0);
+    const int64_t cost = rounds * (P / 128 + 4) + (np > 1 ? 1 : 0);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = P;
     }
+    if (P == 128) break;
   }
   return best;
 }
@@ -654,7 +658,8 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
     if (rule != nullptr && (G == 4 || G == 8) && max_query_len <= 64 / G) {
       const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
       partition_size = auto_partition_few(
-          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), span);
+          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), span,
+          max_context_len);
     } else {
       partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len,
                                             dtype, span);
