@@ -741,6 +741,8 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
   // the query-major kernel decides per block of kMqRows / G query tokens.
   const bool token_major = pa::decode_mq_tc_supported(a);
   a.direct_qblock = token_major ? max_query_len : pa::kMqTiles * (pa::kMqRows / G);
+  // (under a rule its run is always the whole sequence's query tokens)
+  if (token_major && rule != nullptr) a.direct_qblock = 1 << 30;
   const int err = token_major ? pa::launch_decode_mq_tc(a, status, stream)
                               : pa::launch_decode_mq(a, status, stream);
   pa_status st = launch_status(fn, err, 1);
