@@ -234,7 +234,8 @@ struct PartitionParams {
 //     nothing per cache element;
 //   kScoreRule    capped, distance-biased, windowed scores (pa_rule.cuh): the
 //     sequence is taken from the block of its first visible key on, as if the
-//     tokens before were not there.
+//     tokens before were not there.  HBM-bound as the plain kernel (64 sequences
+//     of 40 heads under a distance bias, 1.41 GB: 220 us, 6.4 TB/s).
 enum Mode { kPlain = 0, kBlockScales = 1, kScoreRule = 2 };
 
 template <typename TQ, typename TK, int D, int G, int NCW, int BUDGET, int TPW_, int MODE = kPlain>

@@ -16,21 +16,23 @@
 // first: a bias that grows with distance then puts the largest scores first,
 // and the running maximum, set by the first tiles, hardly rises again (from the
 // first key on, 72 % of the tiles of the chunks below raised it and rescaled O).
-// Each row has ONE softmax thread, which reads its 128
-// scores from TMEM once and keeps them in registers: maximum, rule, exponentials
-// and sum touch nothing else, and no two threads have to agree on a row's
-// maximum (decode_mq.cu's two threads per row read S twice and meet at a barrier
-// every tile; with the rule's work added that took 805 us on 512-token chunks of
-// 8 sequences, 332 GFLOP).  The commit of S_X (i) also covers O_X (i - 1), which
-// was issued before it, so a raised maximum rescales O without another wait.
+// Each row has ONE softmax thread, which reads its 128 scores from TMEM once and
+// keeps them in registers: maximum, rule, exponentials and sum touch nothing
+// else, and no two threads have to agree on a row's maximum (decode_mq.cu's two
+// threads per row read S twice and meet at a barrier every tile; with the rule's
+// work added that took 805 us on 512-token chunks of 8 sequences, 332 GFLOP,
+// where this kernel takes 383: 0.53 of the bf16 peak).  P goes to the tensor
+// core in two halves.  The commit of S_X (i) also covers O_X (i - 1), which was
+// issued before it, so a raised maximum rescales O without another wait.
 //
 // Roles (12 warps): warps 0-3 the first block's softmax and epilogue, warps 4-7
-// the second's, warp 8 TMA producer (Q, then the K/V tiles), warp 9 TMEM owner and MMA
-// issuer (its warpgroup hands its registers to the softmax).  A ring of four K/V
-// tiles and the two Q blocks, 193 KB of shared memory: one CTA per SM.  The CTAs of one kv
-// head's runs are neighbours in the grid and read its K/V from L2.  Every wait
-// is bounded; block ids outside the pool are skipped and flagged; inconsistent
-// query offsets are flagged (PA_DEVERR_CONTEXT) and their sequence skipped.
+// the second's, warp 8 TMA producer (Q, then the K/V tiles), warp 9 TMEM owner
+// and MMA issuer (its warpgroup hands its registers to the softmax).  A ring of
+// four K/V tiles and the two Q blocks, 193 KB of shared memory: one CTA per SM.
+// The CTAs of one kv head's runs are neighbours in the grid and read its K/V
+// from L2.  Every wait is bounded; block ids outside the pool are skipped and
+// flagged; inconsistent query offsets are flagged (PA_DEVERR_CONTEXT) and their
+// sequence skipped.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -96,7 +98,8 @@ __device__ __forceinline__ void fma2(float& x, float& y, float m, float c, float
 // issuer's give up (launch: 384 threads of 168; 2 * 128 * 224 + 128 * 40 = 62464
 // of its 64512).
 constexpr int REGS_SOFTMAX = 224, REGS_OTHER = 40;
-static_assert(NT * 128 * REGS_SOFTMAX + 128 * REGS_OTHER <= 168 * THREADS, "register shares");
+constexpr int REGS_LAUNCH = 168;               // per thread, checked before a launch
+static_assert(NT * 128 * REGS_SOFTMAX + 128 * REGS_OTHER <= REGS_LAUNCH * THREADS, "register shares");
 template <int N>
 __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -291,127 +294,127 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (warp >= 4 * NT) {
-  fewer_registers<REGS_OTHER>();
-  if (warp == 4 * NT) {
-    // ================= producer =================
-    const int row_stride = p.Hkv * bs;
-    bool ok = true;
-    int issued = 0;
-    auto table = [&](int i) {
-      const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
-      return (i < n_tiles && lane < min(bpt, last_blk - b0)) ? __ldg(trow + b0 + lane) : -1;
-    };
-    int pb_next = table(0);
-    for (int i = 0; i < n_tiles && ok; ++i) {
-      const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
-      const int nb = min(bpt, last_blk - b0);
-      const int pb = pb_next;
-      pb_next = table(i + 1);
-      const bool mine = lane < nb;
-      const bool valid = mine && pb >= 0 && pb < p.num_blocks;
-      if (mine && !valid) atomicOr(p.status, PA_DEVERR_TABLE);
-      const unsigned vmask = __ballot_sync(FULL, valid);
-      const uint32_t bytes = __popc(vmask) * 2u * static_cast<uint32_t>(bs) * 128u;
-      const int grp = valid ? (pb * row_stride + g * bs) / 8 : 0;
-      for (int kv = 0; kv < 2; ++kv) {
-        const int u = 2 * i + kv;
-        const int s = u % SLOTS;
-        if (u >= SLOTS && !mbar_wait(&ring_empty[s], ((u / SLOTS) - 1) & 1, p.status)) {
-          ok = false;
-          break;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&ring_full[s], bytes);
-        __syncwarp();
-        if (valid)
-          tma_load_4d(ring + s * SLOT_BYTES + lane * bs * 256, kv == 0 ? &tmap_k : &tmap_v, 0, 0,
-                      0, grp, &ring_full[s]);
-        issued = u + 1;
-      }
-    }
-    if (!ok) {
-      for (int u = issued - SLOTS < 0 ? 0 : issued - SLOTS; u < issued; ++u)
-        mbar_wait(&ring_full[u % SLOTS], (u / SLOTS) & 1, p.status);
-    }
-  } else if (warp == 4 * NT + 1) {
-    // ================= MMA issuer =================
-    if (lane == 0) {
-      const uint32_t id_s = idesc_mq<T>(false);
-      const uint32_t id_o = idesc_mq<T>(true);
-      const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qop);
-      auto issue_s = [&](int x, int i) {           // S_x = Q_x . K_i^T
-        const int s = (2 * i) % SLOTS;
-        const uint32_t d = tmem + x * 128;
-#pragma unroll
-        for (int k = 0; k < DH / 16; ++k) {
-          const uint64_t a =
-              smem_desc(q_a + x * OPA_BYTES + (k >> 2) * OPA_HALF + (k & 3) * 32, 16, 1024);
-          const uint64_t bk =
-              smem_desc(ring_a + s * SLOT_BYTES + (k >> 2) * HALF_OFF + (k & 3) * 32, 16, GROUP_BYTES);
-          mma_f16(d, a, bk, id_s, k > 0);
-        }
-        mma_commit(&s_full[x]);
+    fewer_registers<REGS_OTHER>();
+    if (warp == 4 * NT) {
+      // ================= producer =================
+      const int row_stride = p.Hkv * bs;
+      bool ok = true;
+      int issued = 0;
+      auto table = [&](int i) {
+        const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
+        return (i < n_tiles && lane < min(bpt, last_blk - b0)) ? __ldg(trow + b0 + lane) : -1;
       };
-      auto issue_pv = [&](int x, int i, int h) {   // O_x += P_x . V_i over half h's keys, P_x in TMEM
-        const int s = (2 * i + 1) % SLOTS;
-        const uint32_t d = tmem + 256 + x * 128;
-#pragma unroll
-        for (int k = 4 * h; k < 4 * h + 4; ++k) {
-          const uint64_t bv =
-              smem_desc(ring_a + s * SLOT_BYTES + k * 2 * GROUP_BYTES, HALF_OFF, GROUP_BYTES);
-          mma_f16_ts(d, tmem + x * 128 + k * 8, bv, id_o, (i > 0 || k > 0) ? 1u : 0u);
-        }
-      };
-      auto ring_wait = [&](int u) { return mbar_wait(&ring_full[u % SLOTS], (u / SLOTS) & 1, p.status); };
-      bool ok = mbar_wait(q_ready, 0, p.status) && ring_wait(0);
-      if (ok) {
-        tc_fence_after();
-        issue_s(0, 0);
-        issue_s(1, 0);
-        mma_commit(&ring_empty[0]);
-      }
+      int pb_next = table(0);
       for (int i = 0; i < n_tiles && ok; ++i) {
-        const bool more = i + 1 < n_tiles;
-        ok = ring_wait(2 * i + 1) && mbar_wait(&p_half[0], i & 1, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(0, i, 0);
-        ok = mbar_wait(&p_full[0], i & 1, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(0, i, 1);
-        if (more) {
-          ok = ring_wait(2 * i + 2);
+        const int b0 = first_blk + (n_tiles - 1 - i) * bpt;
+        const int nb = min(bpt, last_blk - b0);
+        const int pb = pb_next;
+        pb_next = table(i + 1);
+        const bool mine = lane < nb;
+        const bool valid = mine && pb >= 0 && pb < p.num_blocks;
+        if (mine && !valid) atomicOr(p.status, PA_DEVERR_TABLE);
+        const unsigned vmask = __ballot_sync(FULL, valid);
+        const uint32_t bytes = __popc(vmask) * 2u * static_cast<uint32_t>(bs) * 128u;
+        const int grp = valid ? (pb * row_stride + g * bs) / 8 : 0;
+        for (int kv = 0; kv < 2; ++kv) {
+          const int u = 2 * i + kv;
+          const int s = u % SLOTS;
+          if (u >= SLOTS && !mbar_wait(&ring_empty[s], ((u / SLOTS) - 1) & 1, p.status)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&ring_full[s], bytes);
+          __syncwarp();
+          if (valid)
+            tma_load_4d(ring + s * SLOT_BYTES + lane * bs * 256, kv == 0 ? &tmap_k : &tmap_v, 0, 0,
+                        0, grp, &ring_full[s]);
+          issued = u + 1;
+        }
+      }
+      if (!ok) {
+        for (int u = issued - SLOTS < 0 ? 0 : issued - SLOTS; u < issued; ++u)
+          mbar_wait(&ring_full[u % SLOTS], (u / SLOTS) & 1, p.status);
+      }
+    } else if (warp == 4 * NT + 1) {
+      // ================= MMA issuer =================
+      if (lane == 0) {
+        const uint32_t id_s = idesc_mq<T>(false);
+        const uint32_t id_o = idesc_mq<T>(true);
+        const uint32_t ring_a = smem_addr(ring), q_a = smem_addr(qop);
+        auto issue_s = [&](int x, int i) {           // S_x = Q_x . K_i^T
+          const int s = (2 * i) % SLOTS;
+          const uint32_t d = tmem + x * 128;
+#pragma unroll
+          for (int k = 0; k < DH / 16; ++k) {
+            const uint64_t a =
+                smem_desc(q_a + x * OPA_BYTES + (k >> 2) * OPA_HALF + (k & 3) * 32, 16, 1024);
+            const uint64_t bk =
+                smem_desc(ring_a + s * SLOT_BYTES + (k >> 2) * HALF_OFF + (k & 3) * 32, 16, GROUP_BYTES);
+            mma_f16(d, a, bk, id_s, k > 0);
+          }
+          mma_commit(&s_full[x]);
+        };
+        auto issue_pv = [&](int x, int i, int h) {   // O_x += P_x . V_i over half h's keys, P_x in TMEM
+          const int s = (2 * i + 1) % SLOTS;
+          const uint32_t d = tmem + 256 + x * 128;
+#pragma unroll
+          for (int k = 4 * h; k < 4 * h + 4; ++k) {
+            const uint64_t bv =
+                smem_desc(ring_a + s * SLOT_BYTES + k * 2 * GROUP_BYTES, HALF_OFF, GROUP_BYTES);
+            mma_f16_ts(d, tmem + x * 128 + k * 8, bv, id_o, (i > 0 || k > 0) ? 1u : 0u);
+          }
+        };
+        auto ring_wait = [&](int u) { return mbar_wait(&ring_full[u % SLOTS], (u / SLOTS) & 1, p.status); };
+        bool ok = mbar_wait(q_ready, 0, p.status) && ring_wait(0);
+        if (ok) {
+          tc_fence_after();
+          issue_s(0, 0);
+          issue_s(1, 0);
+          mma_commit(&ring_empty[0]);
+        }
+        for (int i = 0; i < n_tiles && ok; ++i) {
+          const bool more = i + 1 < n_tiles;
+          ok = ring_wait(2 * i + 1) && mbar_wait(&p_half[0], i & 1, p.status);
           if (!ok) break;
           tc_fence_after();
-          issue_s(0, i + 1);                       // over P_0, which O_0 has read by then
-        } else {
-          mma_commit(&o_full[0]);
-        }
-        ok = mbar_wait(&p_half[1], i & 1, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(1, i, 0);
-        ok = mbar_wait(&p_full[1], i & 1, p.status);
-        if (!ok) break;
-        tc_fence_after();
-        issue_pv(1, i, 1);
-        mma_commit(&ring_empty[(2 * i + 1) % SLOTS]);
-        if (more) {
-          issue_s(1, i + 1);
-          mma_commit(&ring_empty[(2 * i + 2) % SLOTS]);
-        } else {
-          mma_commit(&o_full[1]);
+          issue_pv(0, i, 0);
+          ok = mbar_wait(&p_full[0], i & 1, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(0, i, 1);
+          if (more) {
+            ok = ring_wait(2 * i + 2);
+            if (!ok) break;
+            tc_fence_after();
+            issue_s(0, i + 1);                       // over P_0, which O_0 has read by then
+          } else {
+            mma_commit(&o_full[0]);
+          }
+          ok = mbar_wait(&p_half[1], i & 1, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, i, 0);
+          ok = mbar_wait(&p_full[1], i & 1, p.status);
+          if (!ok) break;
+          tc_fence_after();
+          issue_pv(1, i, 1);
+          mma_commit(&ring_empty[(2 * i + 1) % SLOTS]);
+          if (more) {
+            issue_s(1, i + 1);
+            mma_commit(&ring_empty[(2 * i + 2) % SLOTS]);
+          } else {
+            mma_commit(&o_full[1]);
+          }
         }
       }
+      __syncwarp();
+      // every softmax warp is done with TMEM
+      named_sync(1, NT * 128 + 32);
+      tc_fence_after();
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "r"(TMEM_COLS)
+                   : "memory");
     }
-    __syncwarp();
-    // every softmax warp is done with TMEM
-    named_sync(1, NT * 128 + 32);
-    tc_fence_after();
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(TMEM_COLS)
-                 : "memory");
-  }
   } else {
     more_registers<REGS_SOFTMAX>();
     // ================= softmax: thread of block X, row r (its TMEM lane) =================
@@ -572,6 +575,13 @@ __global__ void __launch_bounds__(THREADS, 1)
 template <typename T, int RULE, bool SLOPES>
 cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream) {
   auto kern = decode_mq_rule_kernel<T, RULE, SLOPES>;
+  // the register shares count on what the kernel was compiled to (a property of
+  // the code, read once); a smaller pool would leave a warpgroup waiting
+  static const int regs = [&] {
+    cudaFuncAttributes at;
+    return cudaFuncGetAttributes(&at, kern) == cudaSuccess ? at.numRegs : 0;
+  }();
+  if (regs < REGS_LAUNCH) return cudaErrorInvalidConfiguration;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv, mq;

