@@ -655,7 +655,7 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
       max_query_len > 0 && num_seqs >= 0)
   {
     const int G = num_heads / num_kv_heads;
-    if (rule != nullptr && (G == 4 || G == 8) && max_query_len <= 64 / G) {
+    if (rule != nullptr && pa::mq_token_major(G, max_query_len, true)) {
       const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
       partition_size = auto_partition_few(
           static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), span,

@@ -219,6 +219,9 @@ struct PartitionParams {
   // by its group (nullable = 0); this launch's partials start at slot_base
   const int32_t* seq_shift;
   int slot_base;
+  // CTAs that share a kv head, each with G of its query heads (kBlockScales and
+  // kScoreRule; their K/V reads meet in L2)
+  int split;
   // kBlockScales: one scale per (physical block, kv head), [NB][Hkv]
   const float* k_scales;
   const float* v_scales;
@@ -253,6 +256,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
 
   const int b = blockIdx.x;
   const int g = blockIdx.y;
+  const int kv = MODE == kPlain ? g : g / p.split;   // kv head
   const int part = blockIdx.z;
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
     const int first_blk = start / bs;
     const int last_blk = (end + bs - 1) / bs;         // exclusive
     const uint32_t blk_bytes = static_cast<uint32_t>(bs) * C::ROW_BYTES;
-    const int64_t head_off = static_cast<int64_t>(g) * blk_bytes;
+    const int64_t head_off = static_cast<int64_t>(kv) * blk_bytes;
     const int64_t blk_stride = static_cast<int64_t>(p.Hkv) * blk_bytes;
     const int32_t* trow =
         p.block_tables + static_cast<int64_t>(b) * p.max_blocks + shift / p.block_size;
@@ -424,7 +428,7 @@ __global__ void __launch_bounds__(Cfg<TK, D, G, NCW, BUDGET, TPW_>::THREADS)
   };
   auto scales_of = [&](int pb) {
     const bool in = pb >= 0 && pb < p.num_blocks;
-    const int64_t at = static_cast<int64_t>(in ? pb : 0) * p.Hkv + g;
+    const int64_t at = static_cast<int64_t>(in ? pb : 0) * p.Hkv + kv;
     ks_next = in ? __ldcg(p.k_scales + at) : 1.f;
     vs_next = in ? __ldcg(p.v_scales + at) : 1.f;
   };
@@ -800,7 +804,8 @@ constexpr int warp_tokens() {
 }
 
 template <typename TQ, typename TK, int D, int G, int BUDGET, int TPW_, int MODE>
-cudaError_t launch_partition_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream) {
+cudaError_t launch_partition_t(const DecodeArgs& a, unsigned int* status, cudaStream_t stream,
+                               int split = 1) {
   constexpr int NCW = consumer_warps<TK, G>();
   using C = Cfg<TK, D, G, NCW, BUDGET, TPW_>;
   auto kern = decode_partition_kernel<TQ, TK, D, G, NCW, BUDGET, TPW_, MODE>;
@@ -830,11 +835,12 @@ cudaError_t launch_partition_t(const DecodeArgs& a, unsigned int* status, cudaSt
   p.v_scale = a.v_scale;
   p.seq_shift = a.seq_shift;
   p.slot_base = a.slot_base;
+  p.split = split;
   p.k_scales = a.k_scales;
   p.v_scales = a.v_scales;
   p.rule = make_rule(a.rule, a.scale);
   if (MODE == kScoreRule) p.scale_log2 = p.rule.scale;
-  dim3 grid(a.num_seqs, a.Hkv, a.num_partitions - a.slot_base);
+  dim3 grid(a.num_seqs, a.Hkv * split, a.num_partitions - a.slot_base);
   return launch_overlapped(kern, grid, dim3(C::THREADS), C::SMEM, stream, p);
 }
 
@@ -845,7 +851,15 @@ cudaError_t launch_partition_g(const DecodeArgs& a, unsigned int* status, cudaSt
     case 1: return launch_partition_t<TQ, TK, D, 1, B, warp_tokens<TK, 1>(), MODE>(a, status, stream);
     case 2: return launch_partition_t<TQ, TK, D, 2, B, warp_tokens<TK, 2>(), MODE>(a, status, stream);
     case 4: return launch_partition_t<TQ, TK, D, 4, B, 8, MODE>(a, status, stream);
-    case 8: return launch_partition_t<TQ, TK, D, 8, B, 8, MODE>(a, status, stream);
+    case 8:
+      // Eight heads take up to 230 registers a thread, one CTA per SM: two CTAs of
+      // four heads each do better though both widen every element (E4M3 codes,
+      // head size 64, 1.15 GB at 128: 1328 -> 828 us; f32 under a window of 4096,
+      // 386 -> 251 us; four of two heads 1441 and 343).
+      if constexpr (MODE != kPlain)
+        return launch_partition_t<TQ, TK, D, 4, B, 8, MODE>(a, status, stream, 2);
+      else
+        return launch_partition_t<TQ, TK, D, 8, B, 8, MODE>(a, status, stream);
     default: return cudaErrorInvalidValue;
   }
 }

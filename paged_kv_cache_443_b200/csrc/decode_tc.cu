@@ -994,6 +994,14 @@ template <typename T, int RULE>
 cudaError_t launch_tcq_g(const MqArgs& m, unsigned int* status, cudaStream_t stream) {
   const int G = m.Hq / m.Hkv;
   const int nq = tc_query_tokens_per_cta(G, m.max_query_len);
+  if constexpr (RULE != kNoRule) {
+    if (G == 1)
+      return nq == 8 ? launch_tcq_t<T, 1, 8, 16, RULE>(m, status, stream)
+                     : launch_tcq_t<T, 1, 16, 16, RULE>(m, status, stream);
+    if (G == 2)
+      return nq == 4 ? launch_tcq_t<T, 2, 4, 16, RULE>(m, status, stream)
+                     : launch_tcq_t<T, 2, 8, 16, RULE>(m, status, stream);
+  }
   if (G == 8) {
     return nq == 2 ? launch_tcq_t<T, 8, 2, 16, RULE>(m, status, stream)
                    : launch_tcq_t<T, 8, 4, 32, RULE>(m, status, stream);
@@ -1009,8 +1017,8 @@ bool decode_mq_tc_supported(const MqArgs& m) {
   const int G = m.Hkv > 0 ? m.Hq / m.Hkv : 0;
   // up to 64 (query token, head) columns, in one or two CTAs per sequence;
   // longer query runs are prefill-like
-  return (m.dtype == PA_F16 || m.dtype == PA_BF16) && m.D == DH && (G == 4 || G == 8) &&
-         m.max_query_len >= 1 && m.max_query_len * G <= 64 && m.partition_size % TOK == 0 &&
+  return (m.dtype == PA_F16 || m.dtype == PA_BF16) && m.D == DH && m.max_query_len >= 1 &&
+         mq_token_major(G, m.max_query_len, m.has_rule) && m.partition_size % TOK == 0 &&
          static_cast<int64_t>(m.num_blocks) * m.Hkv * m.block_size < (int64_t(1) << 31) &&
          encode_fn() != nullptr;
 }

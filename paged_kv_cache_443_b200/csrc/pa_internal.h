@@ -163,10 +163,19 @@ int launch_decode_mq_rule(const MqArgs& a, unsigned int* status, void* stream);
 // token-major tcgen05 decode kernel with per-column causal limits, 16 / G query
 // tokens per CTA (decode_tc.cu).
 bool decode_mq_tc_supported(const MqArgs& a);
+// Whether a call's query tokens are few enough for the token-major kernel: up to
+// 64 (query token, head) columns at G = 4 and 8; under a rule also up to 32 at
+// G = 1 and 2, where the query-major kernel leaves its 128-row blocks nearly
+// empty (178 sequences of 57-102 tokens, 16/8 heads, one query each: 82 -> 40 us).
+inline bool mq_token_major(int G, int max_query_len, bool rule) {
+  if (G == 4 || G == 8) return max_query_len <= 64 / G;
+  return rule && (G == 1 || G == 2) && max_query_len <= 32 / G;
+}
 // Query tokens one CTA of the token-major kernel serves for G query heads per kv
 // head: 2 (G * 2 <= 16 columns), 4 at G = 4 (16 columns), else 32 / G (the
 // N = 32 variant: 4 at G = 8, 8 at G = 4).
 inline int tc_query_tokens_per_cta(int G, int max_query_len) {
+  if (G <= 2) return max_query_len * G <= 8 ? 8 / G : 16 / G;   // under a rule
   if (max_query_len <= 2) return 2;
   if (G == 4 && max_query_len <= 4) return 4;
   return 32 / G;
