@@ -531,7 +531,8 @@ pa_status pa_swap_blocks_fp8_block(void* dst_k_cache, void* dst_v_cache, float* 
  * of its sequence sees, may reach all the sequence's query tokens.
  */
 typedef struct pa_score_rule {
-  float softcap;               /* 0: no cap; else finite and > 0 */
+  float softcap;               /* 0: no cap; else > 0, at most 2^20; a capped score is off by
+                                  up to about softcap * 2^-22 */
   int window;                  /* 0: no window; else the number of last positions seen */
   const float* alibi_slopes;   /* [Hq] float32 (device), or NULL */
   const int32_t* key_starts;   /* [query rows] int32 (device): the first position of the row's
@@ -549,8 +550,8 @@ typedef struct pa_score_rule {
  * the same arguments always suffices.  Partitions count from the first block
  * that a query token sees: with a window the work, the grid and the automatic
  * partition length follow the window, not the context.  PA_ERR_INVALID for a
- * softcap that is negative, not finite, or so small that scale / softcap is not
- * finite, a negative window, or unaligned arrays.
+ * softcap that is negative, NaN, above 2^20, or so small that scale / softcap is
+ * not finite, a negative window, or unaligned arrays.
  */
 pa_status pa_decode_scored(void* out, const void* q, const void* k_cache, const void* v_cache,
                            const int32_t* block_tables, int max_blocks_per_seq,

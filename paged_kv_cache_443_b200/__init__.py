@@ -502,6 +502,10 @@ def _pairs(block_pairs):
     _contig(block_pairs)
     if block_pairs.dtype != torch.int64 or (block_pairs.numel() and block_pairs.shape[-1] != 2):
         raise PagedKVError(PA_ERR_INVALID, "block_pairs must be int64 [P, 2]")
+    if block_pairs.is_cuda:
+        _ready(block_pairs)
+    elif block_pairs.numel() and not block_pairs.is_pinned():   # the GPU reads them
+        raise PagedKVError(PA_ERR_INVALID, "block_pairs must be on the current CUDA device or pinned")
     return (_ptr(block_pairs) if block_pairs.numel() else None), block_pairs.numel() // 2
 
 
@@ -587,6 +591,9 @@ class ScoreRule:
     def __init__(self, softcap: float = 0.0, window: int = 0, alibi_slopes=None, key_starts=None,
                  prefix_lens=None):
         self.softcap, self.window = float(softcap), int(window)
+        if self.softcap and not ctypes.c_float(self.softcap).value:
+            raise PagedKVError(PA_ERR_INVALID, "softcap is too small for a float32")
+        self.window = max(-1, min(self.window, 2 ** 31 - 1))   # a C int: all positions / refused
         self.alibi_slopes, self.key_starts, self.prefix_lens = alibi_slopes, key_starts, prefix_lens
 
     def _struct(self, q, num_seqs: int) -> _ScoreRule:

@@ -225,7 +225,7 @@ pa_status launch_status(const char* fn, int err, int n_launched) {
 pa_status copy_scaled(const char* fn, void* dst_k, void* dst_v, float* dst_ks, float* dst_vs,
                       int dst_blocks, const void* src_k, const void* src_v, const float* src_ks,
                       const float* src_vs, int src_blocks, const int64_t* pairs, int num_pairs,
-                      int num_kv_heads, int head_size, int block_size, void* stream) {
+                      int num_kv_heads, int head_size, int block_size, bool device, void* stream) {
   if (num_pairs < 0) return pa::fail(PA_ERR_INVALID, "%s: num_pairs < 0", fn);
   pa_status st = check_cache_shape(fn, num_kv_heads, head_size, block_size,
                                    dst_blocks < src_blocks ? dst_blocks : src_blocks);
@@ -242,7 +242,7 @@ pa_status copy_scaled(const char* fn, void* dst_k, void* dst_v, float* dst_ks, f
   if (!status) return PA_ERR_CUDA;
   const pa::CopyScaled c = {{dst_k, dst_v},   {src_k, src_v}, {dst_ks, dst_vs}, {src_ks, src_vs},
                             pairs,            num_pairs,      src_blocks,       dst_blocks,
-                            num_kv_heads,     head_size,      block_size,       src_k == dst_k};
+                            num_kv_heads,     head_size,      block_size,       device};
   return launch_status(fn, pa::launch_copy_block_scaled(c, status, stream), 1);
 }
 
@@ -586,8 +586,9 @@ bool rule_active(const pa_score_rule* r) {
 }
 
 pa_status check_rule(const char* fn, const pa_score_rule* r, float scale) {
-  if (!std::isfinite(r->softcap) || r->softcap < 0.f)
-    return pa::fail(PA_ERR_INVALID, "%s: softcap must be 0 or finite and > 0", fn);
+  // above 2^20 a capped score would be off by more than 0.25 (softcap * 2^-22)
+  if (!(r->softcap >= 0.f && r->softcap <= 1048576.f))
+    return pa::fail(PA_ERR_INVALID, "%s: softcap must be in [0, 2^20]", fn);
   if (r->softcap > 0.f && !std::isfinite(4.f * (scale / r->softcap)))
     return pa::fail(PA_ERR_INVALID, "%s: softcap is too small for the scale", fn);
   if (r->window < 0) return pa::fail(PA_ERR_INVALID, "%s: window < 0", fn);
@@ -603,8 +604,8 @@ pa_status check_rule(const char* fn, const pa_score_rule* r, float scale) {
 // a CTA of fixed costs only (128 sequences, 2.06 GB: 335 us, evenly 330).
 int even_partition(int P, int span) {
   if (span <= P) return P;
-  const int np = (span + P - 1) / P;
-  return ((span + np - 1) / np + 127) / 128 * 128;
+  const int64_t np = num_partitions(span, P);
+  return static_cast<int>((span + np - 1) / np + 127) / 128 * 128;
 }
 
 // Partition length for a few query tokens per sequence under a rule (the
@@ -620,10 +621,12 @@ int auto_partition_few(int64_t ctas_per_part, int span, int max_context_len) {
   const int whole = span < 128 ? 128 : (span + 127) / 128 * 128;
   int best = whole;
   int64_t best_cost = -1;
-  for (int want = 1; want <= num_partitions(max_context_len, pa::kDefaultPartition); ++want) {
-    const int P = ((span + want - 1) / want + 127) / 128 * 128;
+  for (int64_t want = 1; want <= num_partitions(max_context_len, pa::kDefaultPartition); ++want) {
+    const int P = static_cast<int>((span + want - 1) / want + 127) / 128 * 128;
     if (P < 128) break;
     const int64_t np = num_partitions(span, P);
+    // np only grows from here, and with it this bound below all that follow
+    if (best_cost >= 0 && ctas_per_part * (span / 128 + 4 * np) >= best_cost * slots) break;
     const int64_t rounds = (ctas_per_part * np + slots - 1) / slots;
     const int64_t cost = rounds * (P / 128 + 4) + (np > 1 ? 1 : 0);
     if (best_cost < 0 || cost < best_cost) {
@@ -905,7 +908,7 @@ extern "C" pa_status pa_swap_blocks_fp8_block(void* dst_k_cache, void* dst_v_cac
   return copy_scaled("pa_swap_blocks_fp8_block", dst_k_cache, dst_v_cache, dst_k_scales,
                      dst_v_scales, dst_num_blocks, src_k_cache, src_v_cache, src_k_scales,
                      src_v_scales, src_num_blocks, block_pairs, num_pairs, num_kv_heads,
-                     head_size, block_size, stream);
+                     head_size, block_size, /*device=*/false, stream);
 }
 
 extern "C" pa_status pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, float* k_scales,
@@ -914,9 +917,8 @@ extern "C" pa_status pa_copy_blocks_fp8_block(void* k_cache, void* v_cache, floa
                                               int block_size, int num_blocks, void* stream) {
   return copy_scaled("pa_copy_blocks_fp8_block", k_cache, v_cache, k_scales, v_scales, num_blocks,
                      k_cache, v_cache, k_scales, v_scales, num_blocks, block_pairs, num_pairs,
-                     num_kv_heads, head_size, block_size, stream);
+                     num_kv_heads, head_size, block_size, /*device=*/true, stream);
 }
-
 
 // ---- shared-prefix groups ----
 

@@ -368,12 +368,12 @@ struct CopyParams {
 };
 
 // Block pairs[p][1] of the destination := block pairs[p][0] of the source, codes
-// and scales, between any memories that the GPU addresses (swap); blockIdx.z selects K or V, a thread moves four 16-byte chunks
-// with all four loads in flight.
+// and scales, between any memories that the GPU addresses (swap); blockIdx.z
+// selects K or V, a thread moves four 16-byte chunks with all four loads in flight.
 __global__ void __launch_bounds__(256) copy_block_scaled_kernel(const CopyParams p) {
   allow_dependents();
   const int kv = blockIdx.z;
-  for (int pr = blockIdx.y; pr < p.num_pairs; pr += gridDim.y) {
+  for (int64_t pr = blockIdx.y; pr < p.num_pairs; pr += gridDim.y) {
     const int64_t src = __ldg(p.pairs + 2 * pr);
     const int64_t dst = __ldg(p.pairs + 2 * pr + 1);
     if (src < 0 || src >= p.src_blocks || dst < 0 || dst >= p.dst_blocks) {

@@ -205,7 +205,7 @@ struct CopyScaled {
   const float* src_scales[2];
   const int64_t* pairs;
   int num_pairs, src_blocks, dst_blocks, Hkv, D, block_size;
-  bool device;   // both pools in device memory (copy-on-write, compaction)
+  bool device;   // one pool in device memory (copy-on-write, compaction)
 };
 int launch_copy_block_scaled(const CopyScaled& c, unsigned int* status, void* stream);
 int launch_copy_blocks(void* dst_k, void* dst_v, const void* src_k, const void* src_v,

@@ -51,7 +51,7 @@ __device__ __forceinline__ void rule_limits(const RuleParams& r, int b, int64_t 
   lo = r.key_starts != nullptr ? max(0, __ldcg(r.key_starts + row)) : 0;
   if (r.window > 0) lo = max(lo, pos - r.window + 1);
   hi = pos;
-  if (r.prefix_lens != nullptr) hi = max(hi, min(__ldcg(r.prefix_lens + b), L) - 1);
+  if (r.prefix_lens != nullptr) hi = max(hi, min(max(__ldcg(r.prefix_lens + b), 0), L) - 1);
 }
 
 // First and last position seen by any of the query tokens i0 .. i1 - 1 of

@@ -87,6 +87,28 @@ BAD_RULES = [
 ]
 
 
+@pytest.mark.parametrize("cap", [1048577.0, 3e38])
+def test_caps_past_the_precision_of_a_score_are_refused(L, cap):
+    assert scored(L, rule=rule(softcap=cap)) == INVALID
+    assert multi(L, rule=rule(softcap=cap)) == INVALID
+
+
+def test_rule_values_past_a_c_type():
+    """A window of more than 2^31 positions is all of them, not what a C int leaves of it;
+    a softcap below the least float32 is not "no cap"."""
+    q = torch.zeros(1, 2, 128)
+    for window, want in ((2 ** 32 + 5, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (-2 ** 32, -1), (7, 7)):
+        assert pk.ScoreRule(window=window)._struct(q, 1).window == want
+    with pytest.raises(pk.PagedKVError):
+        pk.ScoreRule(softcap=1e-60)
+
+
+def test_pairs_that_the_gpu_cannot_read_are_refused():
+    with pytest.raises(pk.PagedKVError):
+        pk._pairs(torch.zeros(1, 2, dtype=torch.int64))
+    assert pk._pairs(torch.zeros(0, 2, dtype=torch.int64)) == (None, 0)
+
+
 @pytest.mark.parametrize("kw,want", COMMON_BAD + [(r, INVALID) for r in BAD_RULES])
 def test_decode_scored_refuses(L, kw, want):
     assert scored(L, **kw) == want and pk.pa_last_error()

@@ -219,6 +219,23 @@ def test_chunks(dtype, group, heads, bs):
         Batch(gen, lens, heads, group, bs, 128, dtype, counts, rule).check(0, 128, 384)
 
 
+def test_extreme_starts_and_prefixes():
+    """The extremes of int32: a prefix of none, a document that has not begun."""
+    gen = torch.Generator().manual_seed(5)
+    least, most = -2 ** 31, 2 ** 31 - 1
+    lens = [400, 60, 300]
+    for counts in ([4, 1, 3], [200, 60, 3]):
+        rows = sum(counts)
+        for rule in (dict(prefix_lens=[least, most, least + 1], window=50),
+                     dict(prefix_lens=[least, -1, most]),
+                     dict(key_starts=[(least, most, 0)[i % 3] for i in range(rows)],
+                          prefix_lens=[least, 20, 0], window=most)):
+            for group in (1, 8):
+                Batch(gen, lens, 1, group, 16, 128, torch.bfloat16, counts, rule).check()
+    Batch(gen, lens, 1, 8, 16, 128, torch.bfloat16,
+          rule=dict(key_starts=[least, most, most - 1], window=most)).check()
+
+
 def test_chunk_rows_of_other_sequences_are_left_alone():
     """A sequence without query tokens, and rows past the last sequence's."""
     gen = torch.Generator().manual_seed(9)
