@@ -2,6 +2,7 @@
 // (all before any launch, so a rejected call has no side effect), workspace
 // sizing and dispatch to the kernel launchers.  See include/pagedkv.h for the
 // contract of every entry point.
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <mutex>
@@ -608,27 +609,32 @@ int even_partition(int P, int span) {
   return static_cast<int>((span + np - 1) / np + 127) / 128 * 128;
 }
 
-// Partition length for a few query tokens per sequence under a rule (the
-// token-major kernel, two CTAs per SM): a CTA's set-up, first running max and
-// epilogue over up to 32 columns cost it about as much as four 128-token tiles,
-// so splitting pays only while it fills idle SMs.  Takes the even split with
-// the fewest (tiles + 4) * rounds of CTAs; the reduce counts as one more tile
-// (64 sequences of 4 tokens, window 1024: three partitions 114 us, two 97, one
-// 66).  Never more partitions than the default length makes of the whole
-// context, which the workspace was sized by.
-int auto_partition_few(int64_t ctas_per_part, int span, int max_context_len) {
-  const int64_t slots = 2ll * num_sms();
-  const int whole = span < 128 ? 128 : (span + 127) / 128 * 128;
-  int best = whole;
+// Partition length for the tensor-core kernels under a rule and over block scales
+// (num_ctas per partition, resident CTAs per SM).  A CTA's set-up, first running
+// max and epilogue cost it about as much as four 128-token tiles, and the reduce
+// with its launch as much as `reduce` tiles, so splitting pays only while it
+// fills idle SMs.  Takes the even split with the least (tiles + 4) * rounds of CTAs:
+// whole rounds where two CTAs share an SM, their exact number where three do
+// (their ends overlap more), at least one.  Never a partition longer than
+// `longest`, nor more of them than the default length makes of the whole context,
+// which the workspace was sized by.  Against lengths chosen by the number of CTAs
+// alone: 64 sequences of 4 tokens under a window of 1024 114 -> 66 us; one token,
+// 64/8 heads, capped, 32 x 250-1000 tokens 31 -> 24, 128 x 500-2000 131 -> 118;
+// block scales 64 x 500-2000 50 -> 40.
+int fewest_rounds(int64_t num_ctas, int per_sm, bool whole_rounds, int reduce, int longest,
+                  int span, int max_context_len) {
+  const int64_t slots = static_cast<int64_t>(per_sm) * num_sms();
+  const int64_t most = num_partitions(max_context_len, pa::kDefaultPartition);
+  int best = pa::kDefaultPartition;
   int64_t best_cost = -1;
-  for (int64_t want = 1; want <= num_partitions(max_context_len, pa::kDefaultPartition); ++want) {
-    const int P = static_cast<int>((span + want - 1) / want + 127) / 128 * 128;
-    if (P < 128) break;
+  for (int64_t want = num_partitions(span, longest); want <= most; ++want) {
+    const int P = std::max(128, static_cast<int>((span + want - 1) / want + 127) / 128 * 128);
     const int64_t np = num_partitions(span, P);
     // np only grows from here, and with it this bound below all that follow
-    if (best_cost >= 0 && ctas_per_part * (span / 128 + 4 * np) >= best_cost * slots) break;
-    const int64_t rounds = (ctas_per_part * np + slots - 1) / slots;
-    const int64_t cost = rounds * (P / 128 + 4) + (np > 1 ? 1 : 0);
+    if (best_cost >= 0 && num_ctas * (span / 128 + 4 * np) >= best_cost) break;
+    const int64_t n = whole_rounds ? (num_ctas * np + slots - 1) / slots * slots
+                                   : std::max(slots, num_ctas * np);
+    const int64_t cost = n * (P / 128 + 4) + (np > 1 ? reduce * slots : 0);
     if (best_cost < 0 || cost < best_cost) {
       best_cost = cost;
       best = P;
@@ -637,6 +643,7 @@ int auto_partition_few(int64_t ctas_per_part, int span, int max_context_len) {
   }
   return best;
 }
+constexpr int kLongestPartition = 4096;
 
 // pa_decode_multi, and with a rule pa_decode_multi_scored.
 pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_cache,
@@ -660,9 +667,9 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
     const int G = num_heads / num_kv_heads;
     if (rule != nullptr && pa::mq_token_major(G, max_query_len, true)) {
       const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
-      partition_size = auto_partition_few(
-          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), span,
-          max_context_len);
+      partition_size = fewest_rounds(
+          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), 2, true,
+          1, std::max(span, 128), span, max_context_len);
     } else {
       partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len,
                                             dtype, span);
@@ -813,9 +820,14 @@ extern "C" pa_status pa_decode_scored(void* out, const void* q, const void* k_ca
       static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
     return pa::fail(PA_ERR_INVALID, "%s: max_context_len %d exceeds max_blocks_per_seq * block_size",
                     fn, max_context_len);
-  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
-    partition_size = even_partition(
-        auto_partition(num_seqs, num_heads, num_kv_heads, head_size, dtype, span), span);
+  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0) {
+    const int G = num_heads / num_kv_heads;
+    if ((dtype == PA_F16 || dtype == PA_BF16) && head_size == 128 && (G == 4 || G == 8))
+      partition_size = fewest_rounds(static_cast<int64_t>(num_seqs) * num_kv_heads, 2, true, 3,
+                                     kLongestPartition, span, max_context_len);
+    else
+      partition_size = even_partition(auto_partition(false, num_seqs, num_kv_heads, span), span);
+  }
   pa::DecodeArgs a;
   st = check_decode_full(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                          context_lens, num_seqs, num_heads, num_kv_heads, head_size, block_size,
@@ -843,11 +855,14 @@ extern "C" pa_status pa_decode_fp8_block(void* out, const void* q, const void* k
                                          int max_context_len, void* workspace,
                                          size_t workspace_bytes_in, void* stream) {
   const char* fn = "pa_decode_fp8_block";
-  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0)   // as pa_decode
-    partition_size = auto_partition(
-        head_size == 128 &&
-            pa::decode_block_on_tc(dtype, num_heads / num_kv_heads, max_context_len),
-        num_seqs, num_kv_heads, max_context_len);
+  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0) {
+    if (head_size == 128 &&
+        pa::decode_block_on_tc(dtype, num_heads / num_kv_heads, max_context_len))
+      partition_size = fewest_rounds(static_cast<int64_t>(num_seqs) * num_kv_heads, 3, false, 3,
+                                     kLongestPartition, max_context_len, max_context_len);
+    else
+      partition_size = auto_partition(false, num_seqs, num_kv_heads, max_context_len);
+  }
   pa::DecodeArgs a;
   pa_status st = check_decode_fp8(fn, out, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                                   context_lens, num_seqs, num_heads, num_kv_heads, head_size,
