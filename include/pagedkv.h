@@ -474,7 +474,8 @@ pa_status pa_decode_partitions_fp8(void* out, const void* q, const void* k_cache
  * slot, race: that block's contents are then unspecified.  One launch.
  *
  * pa_decode_fp8_block: pa_decode over such caches, q and out of type `dtype`
- * (f32 / f16 / bf16), partitions and workspace as pa_decode_fp8.  A scale
+ * (f32 / f16 / bf16), partitions and workspace as pa_decode_fp8 (partition_size
+ * 0: a length of its own, never more partitions than the default's).  A scale
  * outside [2^-40, 2^80] is read as the nearer bound, so one of an all-zero
  * block may hold 0.  Precision as pa_decode_fp8.
  *
