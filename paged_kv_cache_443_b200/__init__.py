@@ -205,7 +205,7 @@ def _contig(*ts):
 def _ready(*ts):
     """Refuses tensors that are not contiguous or not on the current CUDA device
     (kernels run there, on its current stream unless one is given)."""
-    dev = _t().cuda.current_device() if ts[0].is_cuda else -2
+    dev = _t()._C._cuda_getDevice() if ts[0].is_cuda else -2   # CUDA is up then
     for t in ts:
         if t is None:
             continue
@@ -452,7 +452,7 @@ def pa_decode_fp8_block(out, q, k_cache, v_cache, k_scales, v_scales, block_tabl
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, _t().float8_e4m3fn, True)
     _scales(k_cache, k_scales, v_scales)
-    if len(context_lens) != a[7] or len(block_tables) != a[7]:
+    if context_lens.shape[0] != a[7] or block_tables.shape[0] != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
     _check(lib().pa_decode_fp8_block(*a[:4], k_scales.data_ptr(), v_scales.data_ptr(), *a[4:]))
 
@@ -621,7 +621,7 @@ def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale
     _ready(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, None, True)
-    if len(context_lens) != a[7] or len(block_tables) != a[7]:
+    if context_lens.shape[0] != a[7] or block_tables.shape[0] != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
     r = rule._struct(q, a[7])
     _check(lib().pa_decode_scored(*a[:15], ctypes.byref(r), *a[15:]))
