@@ -33,13 +33,68 @@ def _filled(shape, fill: float, dtype: torch.dtype, device) -> torch.Tensor:
     return torch.full(shape, fill, dtype=dtype, device=device)
 
 
+def _other(stream):
+    """`stream` (a torch stream or a raw handle, as the calls take it) as a torch
+    stream; None where it is the current one, or not given."""
+    if stream is None:
+        return None
+    handle = getattr(stream, "cuda_stream", stream)
+    if handle == 1:                # the legacy default stream's other name
+        handle = 0
+    if handle == torch.cuda.current_stream().cuda_stream:
+        return None
+    if handle == 0:
+        return torch.cuda.default_stream()
+    if hasattr(stream, "cuda_stream"):
+        return stream
+    return torch.cuda.ExternalStream(handle, device=torch.cuda.current_device())
+
+
+# Tensors that a launch on `other` (None: on the current stream) needs.  The
+# allocator hands memory out in the order of the stream it was allocated on, so
+# what only the launch touches is allocated on the launch's stream: there it is
+# neither taken from pending work of the current stream nor given to its next
+# tensor while the launch's kernels run.
+def _scratch(other, make):
+    """make(), which allocates what the launch writes and reads."""
+    if other is None:
+        return make()
+    with torch.cuda.stream(other):
+        return make()
+
+
+def _result(other, make):
+    """make(), which allocates what the launch writes and the caller keeps: freed
+    after the current stream's uses of it too."""
+    t = _scratch(other, make)
+    if other is not None:
+        t.record_stream(torch.cuda.current_stream())
+    return t
+
+
+def _uploaded(other, values, device):
+    """`values` as an int64 tensor that the launch reads.  Copied on the current
+    stream; the copy is from pageable memory and done when torch.tensor returns,
+    so `other` has nothing to wait for (nor the host for `other`)."""
+    t = torch.tensor(values, dtype=torch.int64, device=device)
+    if other is not None:
+        t.record_stream(other)
+    return t
+
+
 class PagedKVCache:
     """dtype: the cache's element type, or torch.float8_e4m3fn for a cache of
     E4M3 codes standing for code * k_scale (keys) and code * v_scale (values);
     new K/V and queries are then f32 / f16 / bf16 and quantised on append.
     block_scales: the codes have a scale per (block, kv head) instead
     (self.k_scales, self.v_scales [num_blocks, Hkv] float32), which the append
-    finds; copies and swaps move them with the codes."""
+    finds; copies and swaps move them with the codes.
+
+    The methods that launch take the `stream` to launch on, a torch stream or a
+    raw handle (default: the current one).  What they allocate or upload
+    themselves is safe on any stream; the tensors they are given, and the caches
+    (filled on the stream that was current at their construction), are ordered
+    with that stream and kept alive for it by the caller, as everywhere in torch."""
 
     def __init__(self, num_blocks: int, block_size: int, num_kv_heads: int, head_size: int,
                  dtype: torch.dtype, device="cuda", initial_free_order: Optional[Sequence[int]] = None,
@@ -110,7 +165,7 @@ class PagedKVCache:
         else:
             if not pairs:
                 return
-            t = torch.tensor(pairs, dtype=torch.int64, device=self.device)
+            t = _uploaded(_other(stream), pairs, self.device)
         if not t.numel():
             return
         if self.block_scales:
@@ -121,7 +176,7 @@ class PagedKVCache:
 
     def store(self, key: torch.Tensor, value: torch.Tensor, slot_mapping, stream=None) -> None:
         if not isinstance(slot_mapping, torch.Tensor):
-            slot_mapping = torch.tensor(slot_mapping, dtype=torch.int64, device=self.device)
+            slot_mapping = _uploaded(_other(stream), slot_mapping, self.device)
         if not slot_mapping.numel():
             return
         if self.block_scales:
@@ -184,12 +239,13 @@ class PagedKVCache:
             raise ValueError("a score rule needs a 16-bit or f32 cache and no groups")
         if groups is not None and self.block_scales:
             raise ValueError("groups need a cache without block scales")
+        other = _other(stream)
         if out is None:
-            out = torch.empty_like(q)
+            out = _result(other, lambda: torch.empty_like(q))
         if groups is not None:
             if workspace is None:
-                workspace = self.grouped_workspace(q.shape[0], q.shape[1], max_context_len,
-                                                   groups, partition_size)
+                workspace = _scratch(other, lambda: self.grouped_workspace(
+                    q.shape[0], q.shape[1], max_context_len, groups, partition_size))
             if self.fp8:
                 pa_decode_grouped_fp8(out, q, self.k_cache, self.v_cache, block_tables,
                                       context_lens, groups, scale, max_context_len, self.k_scale,
@@ -201,7 +257,8 @@ class PagedKVCache:
                                   workspace=workspace, stream=stream)
             return out
         if workspace is None:
-            workspace = self.workspace(q.shape[0], q.shape[1], max_context_len, partition_size)
+            workspace = _scratch(other, lambda: self.workspace(q.shape[0], q.shape[1],
+                                                               max_context_len, partition_size))
         if rule is not None:
             pa_decode_scored(out, q, self.k_cache, self.v_cache, block_tables, context_lens,
                              scale, max_context_len, rule, partition_size=partition_size,
@@ -230,12 +287,15 @@ class PagedKVCache:
         """Several query tokens per sequence (its last tokens, already appended):
         q [total_q, Hq, D], query_start_loc [B + 1]; 16-bit caches; with `rule`
         the scores follow it."""
+        other = _other(stream)
         if out is None:
-            out = torch.empty_like(q)
+            out = _result(other, lambda: torch.empty_like(q))
         if workspace is None:
             n = pa_decode_multi_workspace_bytes(q.shape[0], q.shape[1], self.head_size,
                                                 max_context_len, partition_size)
-            workspace = torch.empty(n // 4, dtype=torch.float32, device=self.device) if n else None
+            if n:
+                workspace = _scratch(other, lambda: torch.empty(n // 4, dtype=torch.float32,
+                                                                device=self.device))
         args = (out, q, self.k_cache, self.v_cache, block_tables, context_lens, query_start_loc,
                 scale, max_context_len, max_query_len)
         if rule is not None:
@@ -267,7 +327,7 @@ class PagedKVCache:
     def _move(self, src_alloc, dst_alloc, src_caches, dst_caches, seq_ids, stream):
         pairs = src_alloc.move_to(dst_alloc, seq_ids)    # host: sharing kept, all or nothing
         if pairs:
-            t = torch.tensor(pairs, dtype=torch.int64, device=self.device)
+            t = _uploaded(_other(stream), pairs, self.device)
             if self.block_scales:
                 pa_swap_blocks_fp8_block(*dst_caches, *src_caches, t, stream=stream)
             else:
