@@ -665,13 +665,14 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
       max_query_len > 0 && num_seqs >= 0)
   {
     const int G = num_heads / num_kv_heads;
+    const int seqs = std::max(num_seqs, 1);   // an empty batch: the length for one sequence
     if (rule != nullptr && pa::mq_token_major(G, max_query_len, true)) {
       const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
       partition_size = fewest_rounds(
-          static_cast<int64_t>(num_seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), 2, true,
+          static_cast<int64_t>(seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), 2, true,
           1, std::max(span, 128), span, max_context_len);
     } else {
-      partition_size = auto_partition_multi(num_seqs, num_heads, num_kv_heads, max_query_len,
+      partition_size = auto_partition_multi(seqs, num_heads, num_kv_heads, max_query_len,
                                             dtype, span);
     }
   }
