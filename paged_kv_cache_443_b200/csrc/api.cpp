@@ -653,28 +653,9 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
                        int head_size, int block_size, int num_blocks, float scale, pa_dtype dtype,
                        const pa_score_rule* rule, int partition_size, int max_context_len,
                        void* workspace, size_t workspace_bytes_in, void* stream) {
-  // keys that a run of query tokens can span (the whole context without a window)
-  int span = max_context_len;
   if (rule != nullptr) {
     const pa_status rs = check_rule(fn, rule, scale);
     if (rs != PA_OK) return rs;
-    if (max_query_len > 0 && block_size > 0)
-      span = pa::rule_span_bound(*rule, max_context_len, max_query_len, block_size);
-  }
-  if (partition_size == 0 && num_heads > 0 && num_kv_heads > 0 && num_heads % num_kv_heads == 0 &&
-      max_query_len > 0 && num_seqs >= 0)
-  {
-    const int G = num_heads / num_kv_heads;
-    const int seqs = std::max(num_seqs, 1);   // an empty batch: the length for one sequence
-    if (rule != nullptr && pa::mq_token_major(G, max_query_len, true)) {
-      const int nq = pa::tc_query_tokens_per_cta(G, max_query_len);
-      partition_size = fewest_rounds(
-          static_cast<int64_t>(seqs) * num_kv_heads * ((max_query_len + nq - 1) / nq), 2, true,
-          1, std::max(span, 128), span, max_context_len);
-    } else {
-      partition_size = auto_partition_multi(seqs, num_heads, num_kv_heads, max_query_len,
-                                            dtype, span);
-    }
   }
   if (pa::elem_size(dtype) == 0) return pa::fail(PA_ERR_INVALID, "%s: unknown dtype %d", fn, dtype);
   if (dtype != PA_F16 && dtype != PA_BF16)
@@ -690,6 +671,23 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
     return pa::fail(PA_ERR_INVALID, "%s: sizes must be positive", fn);
   if (!supported_block(block_size))
     return pa::fail(PA_ERR_UNSUPPORTED, "%s: block_size must be 8, 16 or 32", fn);
+  const int G = num_heads / num_kv_heads;
+  // What an empty batch gives does not matter, but its sizes must not: it is taken
+  // as one sequence of at least one query token.
+  const int seqs = std::max(num_seqs, 1);
+  const int run = std::max(1, std::min(max_query_len, max_context_len));
+  // keys that a run of query tokens can span (the whole context without a window)
+  const int span = rule != nullptr ? pa::rule_span_bound(*rule, max_context_len, run, block_size)
+                                   : max_context_len;
+  if (partition_size == 0) {
+    if (rule != nullptr && pa::mq_token_major(G, run, true)) {
+      const int nq = pa::tc_query_tokens_per_cta(G, run);
+      partition_size = fewest_rounds(static_cast<int64_t>(seqs) * num_kv_heads * ((run + nq - 1) / nq),
+                                     2, true, 1, std::max(span, 128), span, max_context_len);
+    } else {
+      partition_size = auto_partition_multi(seqs, num_heads, num_kv_heads, run, dtype, span);
+    }
+  }
   const int P = resolve_partition(partition_size);
   if (P < 0 || P % 128 != 0)
     return pa::fail(PA_ERR_INVALID, "%s: partition_size must be 0 or a positive multiple of 128", fn);
@@ -700,7 +698,6 @@ pa_status decode_multi(const char* fn, void* out, const void* q, const void* k_c
     return pa::fail(PA_ERR_INVALID, "%s: max_query_len must be in [1, min(total_q, max_context_len)]", fn);
   if (!std::isfinite(scale)) return pa::fail(PA_ERR_INVALID, "%s: scale is not finite", fn);
   const int64_t NP = num_partitions(span, P);
-  const int G = num_heads / num_kv_heads;
   const int64_t qblocks = total_q > 0 ? (max_query_len + pa::kMqRows / G - 1) / (pa::kMqRows / G) : 0;
   const int64_t qpairs = (qblocks + pa::kMqTiles - 1) / pa::kMqTiles;
   if (qpairs * NP > 65535) return pa::fail(PA_ERR_UNSUPPORTED, "%s: too many query blocks x partitions", fn);

@@ -41,3 +41,18 @@ def statuses(**kw):
 def test_an_empty_batch_is_nothing_to_do(window, maxq, ctx, Hq):
     assert statuses(B=0, T=0, maxq=maxq, ctx=ctx, Hq=Hq, window=window) == (pk.PA_OK, pk.PA_OK)
     assert statuses(B=3, T=0, maxq=maxq, ctx=ctx, Hq=Hq, window=window) == (pk.PA_OK, pk.PA_OK)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(256, 1), (1024, 2), (2000, 2), (1 << 20, 8)])
+@pytest.mark.parametrize("B,T,maxq,ctx", [(2, 8, 4, 4096), (0, 0, 512, 4096), (4, 600, 512, 1 << 20)])
+def test_heads_per_kv_head_past_a_query_block_are_refused(Hq, Hkv, B, T, maxq, ctx):
+    want = (pk.PA_ERR_UNSUPPORTED, pk.PA_ERR_UNSUPPORTED)
+    assert statuses(Hq=Hq, Hkv=Hkv, B=B, T=T, maxq=maxq, ctx=ctx) == want
+    assert statuses(Hq=Hq, Hkv=Hkv, B=B, T=T, maxq=maxq, ctx=ctx, window=700) == want
+
+
+@pytest.mark.parametrize("maxq", [2 ** 31 - 1, 2 ** 31 - 127, 0, -5, -2 ** 31])
+@pytest.mark.parametrize("window", [0, 700])
+def test_query_lengths_out_of_range(maxq, window):
+    assert statuses(maxq=maxq, window=window) == (pk.PA_ERR_INVALID, pk.PA_ERR_INVALID)
+    assert statuses(maxq=maxq, window=window, T=0) == (pk.PA_OK, pk.PA_OK)
