@@ -468,10 +468,11 @@ pa_status pa_decode_partitions_fp8(void* out, const void* q, const void* k_cache
  *   call does not write becomes E4M3(code * (old / new)) (for powers of two
  *   exact except where it reaches E4M3's subnormals)
  * Slots of a block started anew that the call does not write keep their bytes.
- * A negative slot is skipped.  The tokens of one block must stand next to each
- * other in slot_mapping (pa_seq_append's slots of one sequence after another's
- * do); two separate runs of one block in a call, or two tokens given the same
- * slot, race: that block's contents are then unspecified.  One launch.
+ * A negative slot is skipped, wherever it stands.  Apart from those the tokens of
+ * one block must stand next to each other in slot_mapping (pa_seq_append's slots
+ * of one sequence after another's do); tokens of another block between them, or
+ * two tokens given the same slot, race: that block's contents are then
+ * unspecified.  One launch.
  *
  * pa_decode_fp8_block: pa_decode over such caches, q and out of type `dtype`
  * (f32 / f16 / bf16), partitions and workspace as pa_decode_fp8 (partition_size

@@ -462,8 +462,9 @@ def pa_reshape_and_cache_fp8_block(key, value, k_cache, v_cache, k_scales, v_sca
     """Store key/value (f32 / f16 / bf16) as E4M3 codes at their slots, finding
     each block's scale: the smallest power of two that holds the block's largest
     element, never below the stored one (a block whose first slot is written
-    starts anew); the block's older codes follow when it grows.  The tokens of a
-    block stand next to each other in slot_mapping."""
+    starts anew); the block's older codes follow when it grows.  Negative slots
+    are skipped; apart from those the tokens of a block stand next to each other
+    in slot_mapping."""
     _ready(key, value, k_cache, v_cache, k_scales, v_scales, slot_mapping)
     torch = _t()
     N, Hkv, D = shape = key.shape

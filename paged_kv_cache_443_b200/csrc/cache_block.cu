@@ -166,21 +166,26 @@ __device__ __forceinline__ void rescale(uint8_t* rows, int bs, unsigned written,
 }
 
 // One warp per (up to 16 positions of slot_mapping, kv head, K or V).  A block's
-// tokens stand next to each other in slot_mapping; the warp that looks after
-// the first of them does them all.  One read of 32 slots tells where the runs
-// begin and end and which offsets they write.
+// tokens form a run of positions, skipped slots among them; the warp that looks
+// after the first of them does them all.  One read of 32 slots tells where the
+// runs begin and end and which offsets they write, except next to skipped slots:
+// the block of the last slot in use before them, and of the next one behind them,
+// is then looked for, the latter while the elements are loaded.
 //   Several runs that end among the positions (a decode or verification step):
 //   all the positions' rows are loaded at once, a row per D / EPL lanes, and a
 //   run's first lane settles its scale.
-//   A run that goes on, or a single one: up to 16 tokens' elements are loaded into
-//   registers (16 bytes per lane and load, all loads in flight together),
+//   A run that goes on, or a single one: up to 16 positions' elements are loaded
+//   into registers (16 bytes per lane and load, all loads in flight together),
 //   their largest found, the scale settled, the codes written.  A run that
 //   goes on past the 32 slots (blocks of 32; a slot given several times) is
-//   followed further, and what is past 16 tokens is read again, from L2.
+//   followed further, and what is past 16 positions is read again, from L2.
 // Bound by memory latency, not bandwidth, until the call has a few thousand
 // tokens: three dependent accesses (slots; elements and scale; codes).
 // Measured (8 kv heads, head size 128, bf16 / f16): 256 tokens 6 us; 24 x 512
-// tokens 21 us (75.7 MB, 3.6 TB/s).
+// tokens 21 us (75.7 MB, 3.6 TB/s).  Padding behind a batch costs its last warps a
+// scan: 100 tokens and 156 skipped slots 5.0 us, 8 and 1000 8.3 us (4.6 and 4.1 if
+// skipped slots ended a run; tokens behind them were then another warp's, and the
+// two raced on the block's scale and codes).
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     append_block_kernel(const AppendParams p) {
@@ -211,28 +216,61 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     return s >= 0 && s < p.num_slots ? static_cast<int>(s >> p.log2_bs) : -1;
   };
   const int64_t slot = slot_at(at0 + lane);
+  const int64_t slot_ahead = __ldg(p.slots + (at0 > 0 ? at0 - 1 : 0));
   const int mine = block_of(slot);
-  int before = __shfl_up_sync(FULL, mine, 1);
-  if (lane == 0) before = block_of(slot_at(at0 - 1));
   const int offset = static_cast<int>(slot) & (bs - 1);
   const bool here = lane < p.positions;
   if (here && h == 0 && kv == 0 && slot >= p.num_slots) atomicOr(p.status, PA_DEVERR_SLOT);
-  unsigned leaders = __ballot_sync(FULL, here && mine >= 0 && mine != before);
+  // A run starts where the last slot in use before it is of another block: skipped
+  // slots do not end one.  `before` is that block for the window's first slot in use.
+  const unsigned used = __ballot_sync(FULL, mine >= 0);
+  int before = at0 > 0 ? block_of(slot_ahead) : -1;
+  if (before < 0 && at0 > 1 && (used & ((1u << p.positions) - 1u)) != 0) {
+#pragma unroll 1
+    for (int64_t i = at0 - 2; before < 0 && i >= 0; i -= 32) {
+      const int b = block_of(slot_at(i - lane));
+      const unsigned in = __ballot_sync(FULL, b >= 0);
+      if (in != 0) before = __shfl_sync(FULL, b, __ffs(in) - 1);
+    }
+  }
+  const unsigned below = used & ((1u << lane) - 1u);
+  int prev = __shfl_sync(FULL, mine, below != 0 ? 31 - __clz(below) : 0);
+  if (below == 0) prev = before;
+  unsigned leaders = __ballot_sync(FULL, here && mine >= 0 && mine != prev);
   uint4 v[IT];
 
+  // the first position from i on whose slot is in use (num_tokens: none); 128 slots
+  // in flight (four loads a lane: eight cost the registers of the paths below)
+  auto next_used = [&](int64_t i) -> int64_t {
+#pragma unroll 1
+    for (; i < p.num_tokens; i += 128) {
+      unsigned m = 0;                        // bit k: position i + 32 k + lane
+#pragma unroll
+      for (int k = 0; k < 4; ++k) m |= block_of(slot_at(i + 32 * k + lane)) >= 0 ? 1u << k : 0u;
+      const unsigned any = __reduce_or_sync(FULL, m);
+      if (any != 0) {
+        const int k = __ffs(any) - 1;
+        return i + 32 * k + __ffs(__ballot_sync(FULL, (m >> k) & 1u)) - 1;
+      }
+    }
+    return p.num_tokens;
+  };
   // The runs that end among the positions, if there are several: all but the
   // last one where that goes on behind them.
-  const bool cross = p.positions < 32 &&
-                     __shfl_sync(FULL, mine >= 0 && mine == before ? 1 : 0, p.positions & 31) != 0;
   const int last = 31 - __clz(leaders);
-  const unsigned many = cross && leaders != 0 ? leaders & ~(1u << last) : leaders;
+  const unsigned later = used >> p.positions;
+  const int next = __shfl_sync(FULL, mine, later != 0 ? p.positions + __ffs(later) - 1 : 0);
+  const int last_block = __shfl_sync(FULL, mine, last & 31);
+  const bool cross = later != 0 && next == last_block;
+  unsigned many = cross && leaders != 0 ? leaders & ~(1u << last) : leaders;
   if ((many & (many - 1)) != 0) {
     // ---- row r = position c0 + r, a member of the run of the leader before it ----
     const int end = cross ? last : p.positions;
     const unsigned upto = many & (0xffffffffu >> (31 - lane));
-    const bool in = lane < end && mine >= 0 && upto != 0;
-    const unsigned rows_in = __ballot_sync(FULL, in);
-    const int lead = in ? 31 - __clz(upto) : lane;
+    const bool member = lane < end && upto != 0;   // or a skipped slot between two
+    const bool in = member && mine >= 0;
+    unsigned rows_in = __ballot_sync(FULL, in);
+    const int lead = member ? 31 - __clz(upto) : lane;
     const int64_t srow = static_cast<int64_t>(in ? mine : 0) * p.Hkv + h;
     float old = in ? fmaxf(__ldcg(scales + srow), 0.f) : 0.f;
     {
@@ -241,6 +279,13 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
       for (int k = 0; k < IT; ++k, src += RPW * x_stride)
         v[k] = (rows_in >> (k * RPW + sub)) & 1u ? __ldg(reinterpret_cast<const uint4*>(src))
                                                  : make_uint4(0, 0, 0, 0);
+    }
+    // nothing but skipped slots in the rest of the window: the last run may go on
+    // behind them and is then not for here
+    if (later == 0 && at0 + 32 < p.num_tokens &&
+        block_of(slot_at(next_used(at0 + 32))) == last_block) {
+      many &= ~(1u << last);
+      rows_in &= (1u << last) - 1u;
     }
     float most = 0.f;                        // of position `lane`
 #pragma unroll
@@ -295,37 +340,71 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     const int at = __ffs(leaders) - 1;
     leaders &= leaders - 1;
     const int blk = __shfl_sync(FULL, mine, at);
-    // ---- the run of positions in this block, and the offsets it writes ----
-    int n = __ffs(~(__ballot_sync(FULL, mine == blk) >> at)) - 1;
-    if (at + n > 32 || n < 0) n = 32 - at;   // up to the last lane
-    unsigned written = __reduce_or_sync(FULL, lane >= at && lane < at + n ? 1u << offset : 0u);
+    // ---- the run's n positions (skipped slots among them), which of the window's and
+    // of the next 32 are its tokens, and the offsets it writes ----
     const int64_t first = static_cast<int64_t>(c0) + at;
-    if (at + n == 32) {
-      for (;;) {                             // past the 32 slots read
-        const int64_t s = slot_at(first + n + lane);
-        const unsigned same = __ballot_sync(FULL, block_of(s) == blk);
-        const int add = same == FULL ? 32 : __ffs(~same) - 1;
-        written |= __reduce_or_sync(
-            FULL, lane < add ? 1u << (static_cast<int>(s) & (bs - 1)) : 0u);
-        n += add;
-        if (add < 32) break;
-      }
-    }
-    const bool fresh = (written & 1u) != 0;
+    unsigned written = 0, other = 0;
+    int n = 0, offset1 = 0;                  // offset1: of position c0 + 32 + lane
+    // its tokens among 32 positions from c0 + from on, up to the next one of another block
+    auto take = [&](int64_t from, int b, int off, unsigned keep) -> unsigned {
+      other = __ballot_sync(FULL, b >= 0 && b != blk) & keep;
+      unsigned m = __ballot_sync(FULL, b == blk) & keep;
+      if (other != 0) m &= (other & (0u - other)) - 1u;
+      written |= __reduce_or_sync(FULL, (m >> lane) & 1u ? 1u << off : 0u);
+      if (m != 0) n = static_cast<int>(from) + 32 - __clz(m) - at;
+      return m;
+    };
     const int64_t row0 = static_cast<int64_t>(blk) * p.Hkv + h;
-    uint8_t* rows = cache + (row0 << p.log2_bs) * D;
-    const float old = fresh ? 0.f : fmaxf(__ldcg(scales + row0), 0.f);
-
-    auto load = [&](int t0) {                // tokens first + t0 ..
+    const float stored = __ldcg(scales + row0);
+    const unsigned tokens0 = take(0, mine, offset, FULL << at);
+    unsigned tokens1 = 0;
+    // lane l < kChunk: whether position first + t0 + l is a token of the run, its offset
+    unsigned rows_in = 0;
+    int off_in = 0;
+    auto look = [&](int t0) {
+      const int w = at + t0 + lane;
+      off_in = __shfl_sync(FULL, offset, w & 31);
+      bool in = w < 32 && ((tokens0 >> (w & 31)) & 1u) != 0;
+      if (at + t0 + kChunk > 32) {
+        const int o = __shfl_sync(FULL, offset1, w & 31);
+        if (w >= 32) {
+          off_in = o;
+          in = w < 64 && ((tokens1 >> (w & 31)) & 1u) != 0;
+          if (w >= 64 && t0 + lane < n) {    // read again, from L1 or L2
+            const int64_t s = __ldg(p.slots + first + t0 + lane);
+            in = block_of(s) == blk;
+            off_in = static_cast<int>(s) & (bs - 1);
+          }
+        }
+      }
+      rows_in = __ballot_sync(FULL, lane < kChunk && in);
+    };
+    auto load = [&](int t0) {                // the tokens among first + t0 ..
+      look(t0);
       const T* src = x + (first + t0 + sub) * x_stride;
 #pragma unroll
       for (int k = 0; k < IT; ++k, src += RPW * x_stride)
-        v[k] = t0 + k * RPW + sub < n ? __ldg(reinterpret_cast<const uint4*>(src))
-                                      : make_uint4(0, 0, 0, 0);
+        v[k] = (rows_in >> (k * RPW + sub)) & 1u ? __ldg(reinterpret_cast<const uint4*>(src))
+                                                 : make_uint4(0, 0, 0, 0);
     };
+    load(0);                                 // in flight while the rest of the run is found
+    if (other == 0 && at0 + 32 < p.num_tokens) {
+      const int64_t s = slot_at(at0 + 32 + lane);
+      offset1 = static_cast<int>(s) & (bs - 1);
+      tokens1 = take(32, block_of(s), offset1, FULL);
+#pragma unroll 1
+      for (int64_t i = at0 + 64; other == 0 && (i = next_used(i)) < p.num_tokens; i += 32) {
+        const int64_t t = slot_at(i + lane);
+        take(i - at0, block_of(t), static_cast<int>(t) & (bs - 1), FULL);
+      }
+    }
+    const bool fresh = (written & 1u) != 0;
+    uint8_t* rows = cache + (row0 << p.log2_bs) * D;
+    const float old = fresh ? 0.f : fmaxf(stored, 0.f);
+
     float most = 0.f;
     for (int t0 = 0; t0 < n; t0 += kChunk) {
-      load(t0);
+      if (t0 > 0) load(t0);
       uint32_t bits = 0;
 #pragma unroll
       for (int k = 0; k < IT; ++k) gather_max<T>(bits, v[k]);
@@ -346,10 +425,9 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
       if (n > kChunk) load(t0);
 #pragma unroll
       for (int k = 0; k < IT; ++k) {
-        const int t = t0 + k * RPW + sub;
-        int off = __shfl_sync(FULL, offset, (at + t) & 31);
-        if (t >= n) continue;
-        if (at + t >= 32) off = static_cast<int>(__ldg(p.slots + first + t)) & (bs - 1);
+        const int r = k * RPW + sub;
+        const int off = __shfl_sync(FULL, off_in, r);
+        if (((rows_in >> r) & 1u) == 0) continue;
         store_codes<T>(v[k], div, rows + off * D + col);
       }
     }
