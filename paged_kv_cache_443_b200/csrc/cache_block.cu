@@ -181,11 +181,11 @@ __device__ __forceinline__ void rescale(uint8_t* rows, int bs, unsigned written,
 //   followed further, and what is past 16 positions is read again, from L2.
 // Bound by memory latency, not bandwidth, until the call has a few thousand
 // tokens: three dependent accesses (slots; elements and scale; codes).
-// Measured (8 kv heads, head size 128, bf16 / f16): 256 tokens 6 us; 24 x 512
+// Measured (8 kv heads, head size 128, bf16 / f16): 256 tokens 4 us; 24 x 512
 // tokens 21 us (75.7 MB, 3.6 TB/s).  Padding behind a batch costs its last warps a
-// scan: 100 tokens and 156 skipped slots 5.0 us, 8 and 1000 8.3 us (4.6 and 4.1 if
-// skipped slots ended a run; tokens behind them were then another warp's, and the
-// two raced on the block's scale and codes).
+// scan: 100 tokens and 156 skipped slots 4.4 us, 8 and 1000 8.0 us (where skipped
+// slots ended a run, 4.6 and 4.1; tokens behind them were then another warp's, and
+// the two raced on the block's scale and codes).
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     append_block_kernel(const AppendParams p) {
@@ -615,13 +615,16 @@ int log2_of(int x) {
   return r;
 }
 
-// List positions a warp looks after (1 .. 16): as many as still give the SMs 16
-// warps each.  Decode steps of 256 / 1024 / 4096 tokens (8 kv heads) take 6 / 8 /
-// 11 us so (one position per warp: 6 / 16 / 46 us).
+// List positions a warp looks after (1 .. 16): as many as still give the SMs six
+// warps each: enough to have the loads of a short call in flight at once, and
+// fewer warps that read the same slots.  Decode steps of 256 / 512 / 1024 / 2048
+// tokens (8 kv heads) take 4.0 / 4.4 / 5.2 / 6.4 us so, 5.9 / 7.7 / 8.2 / 9.0 with
+// sixteen warps each; 4096 tokens 12.0 / 11.7.
 int positions_per_warp(int num_tokens, int Hkv) {
   const int64_t items = static_cast<int64_t>(num_tokens) * Hkv * 2;
+  const int64_t least = 6ll * num_sms();
   int n = 1;
-  while (n < kChunk && items / (2 * n) >= 148 * 16) n *= 2;
+  while (n < kChunk && items / (2 * n) >= least) n *= 2;
   return n;
 }
 
