@@ -459,10 +459,11 @@ pa_status pa_decode_partitions_fp8(void* out, const void* q, const void* k_cache
  *   a    = max |x[t][h][d]| over the call's tokens of the block, NaNs aside
  *   need = the smallest power of two 2^e, -40 <= e <= 80, with a <= 448 * 2^e
  *          (2^80 if none)
- *   old  = scales[i][h] (0 if that is negative or NaN), or 0 if one of the
- *          call's slots is the block's first (offset 0): writing it starts the
- *          block anew
- *   new  = max(old, need)                                  -> scales[i][h]
+ *   old  = scales[i][h] as the decode reads it (within [2^-40, 2^80]; 0 if it is 0,
+ *          negative or NaN), or 0 if one of the call's slots is the block's first
+ *          (offset 0): writing it starts the block anew
+ *   new  = max(old, need)                                  -> scales[i][h], unless
+ *          what is kept there is larger (a caller's own scale above 2^80)
  *   each token's codes: E4M3(fp32(x) / new), as pa_reshape_and_cache_fp8
  *   if new > old and the block is not started anew, each code at an offset the
  *   call does not write becomes E4M3(code * (old / new)) (for powers of two

@@ -9,8 +9,8 @@
 //
 //   a    = max |x| over the call's tokens of the block and head (NaNs aside)
 //   need = the smallest 2^e with a <= 448 * 2^e, -40 <= e <= 80
-//   old  = the stored scale; 0 if the call writes offset 0 of the block, which
-//          starts the block anew
+//   old  = the stored scale, as the decode reads it; 0 if the call writes offset 0
+//          of the block, which starts the block anew
 //   new  = max(old, need);  code = E4M3(x / new), saturating at 448
 //   if new > old > 0: the block's other slots, code := E4M3(code * old / new)
 //
@@ -39,6 +39,14 @@ __device__ __forceinline__ float scale_for(float most) {
   int e = static_cast<int>(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   e = max(-40, min(80, e));
   return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+}
+
+// A stored scale (negative and NaN taken as 0) as the decode kernels read it; 0
+// stays 0, its codes are no tokens yet.  What the append stores is at least the
+// stored one, so one above the bound stays as the caller set it, and its codes are
+// relative to the bound.
+__device__ __forceinline__ float as_read(float stored) {
+  return stored > 0.f ? fminf(fmaxf(stored, kScaleMin), kScaleMax) : 0.f;
 }
 
 __device__ __forceinline__ uint32_t codes2(float a, float b) {
@@ -272,7 +280,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     unsigned rows_in = __ballot_sync(FULL, in);
     const int lead = member ? 31 - __clz(upto) : lane;
     const int64_t srow = static_cast<int64_t>(in ? mine : 0) * p.Hkv + h;
-    float old = in ? fmaxf(__ldcg(scales + srow), 0.f) : 0.f;
+    float stored = in ? fmaxf(__ldcg(scales + srow), 0.f) : 0.f;
     {
       const T* src = x + (static_cast<int64_t>(c0) + sub) * x_stride;
 #pragma unroll
@@ -311,11 +319,12 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
         written |= w;
       }
     }
-    if (written & 1u) old = 0.f;
+    if (written & 1u) stored = 0.f;
+    const float old = as_read(stored);
     float now = fmaxf(old, scale_for(most));
     const bool is_lead = (many >> lane) & 1u;
     unsigned grown = __ballot_sync(FULL, is_lead && !(written & 1u) && now > old);
-    if (is_lead) scales[srow] = now;
+    if (is_lead) scales[srow] = fmaxf(stored, now);
     while (grown) {
       const int at = __ffs(grown) - 1;
       grown &= grown - 1;
@@ -355,7 +364,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
       return m;
     };
     const int64_t row0 = static_cast<int64_t>(blk) * p.Hkv + h;
-    const float stored = __ldcg(scales + row0);
+    const float stored = fmaxf(__ldcg(scales + row0), 0.f);
     const unsigned tokens0 = take(0, mine, offset, FULL << at);
     unsigned tokens1 = 0;
     // lane l < kChunk: whether position first + t0 + l is a token of the run, its offset
@@ -400,7 +409,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     }
     const bool fresh = (written & 1u) != 0;
     uint8_t* rows = cache + (row0 << p.log2_bs) * D;
-    const float old = fresh ? 0.f : fmaxf(stored, 0.f);
+    const float old = fresh ? 0.f : as_read(stored);
 
     float most = 0.f;
     for (int t0 = 0; t0 < n; t0 += kChunk) {
@@ -419,7 +428,7 @@ __global__ void __launch_bounds__(32 * kWarps, sizeof(T) == 4 ? 2 : 3)
     most = __uint_as_float(__reduce_max_sync(FULL, __float_as_uint(most)));   // >= 0: ordered as bits
     const float now = fmaxf(old, scale_for(most));
     if (now > old && !fresh) rescale<D>(rows, bs, written, old, now);
-    if (lane == 0) scales[row0] = now;
+    if (lane == 0) scales[row0] = fresh ? now : fmaxf(stored, now);
     const Divide div = divide_by<T>(now);
     for (int t0 = 0; t0 < n; t0 += kChunk) {
       if (n > kChunk) load(t0);
