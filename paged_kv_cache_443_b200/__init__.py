@@ -616,31 +616,32 @@ class ScoreRule:
 
 
 def pa_decode_scored(out, q, k_cache, v_cache, block_tables, context_lens, scale,
-                     max_context_len, rule: ScoreRule, partition_size=0, workspace=None,
+                     max_context_len, rule: Optional[ScoreRule], partition_size=0, workspace=None,
                      stream=None) -> None:
-    """pa_decode under a score rule (capped, distance-biased, windowed scores)."""
+    """pa_decode under a score rule (capped, distance-biased, windowed scores); None:
+    the plain call."""
     _ready(q, out, k_cache, v_cache, block_tables, context_lens, workspace)
     a = _decode_args(out, q, k_cache, v_cache, block_tables, context_lens, scale, partition_size,
                      max_context_len, workspace, stream, None, True)
     if context_lens.shape[0] != a[7] or block_tables.shape[0] != a[7]:
         raise PagedKVError(PA_ERR_INVALID, "one query, table row and length per sequence")
-    r = rule._struct(q, a[7])
-    _check(lib().pa_decode_scored(*a[:15], ctypes.byref(r), *a[15:]))
+    r = None if rule is None else ctypes.byref(rule._struct(q, a[7]))
+    _check(lib().pa_decode_scored(*a[:15], r, *a[15:]))
 
 
 def pa_decode_multi_scored(out, q, k_cache, v_cache, block_tables, context_lens,
                            query_start_loc, scale, max_context_len, max_query_len,
-                           rule: ScoreRule, partition_size=0, workspace=None,
+                           rule: Optional[ScoreRule], partition_size=0, workspace=None,
                            stream=None) -> None:
     """pa_decode_multi under a score rule, with document starts per query token
-    and prefixes attended in both directions."""
+    and prefixes attended in both directions; None: the plain call."""
     _ready(q, out, k_cache, v_cache, block_tables, context_lens, query_start_loc, workspace)
     a = _multi_args(out, q, k_cache, v_cache, block_tables, context_lens, query_start_loc, scale,
                     max_context_len, max_query_len, partition_size, workspace, stream)
     if block_tables.shape[0] != context_lens.shape[0]:
         raise PagedKVError(PA_ERR_INVALID, "one table row and length per sequence")
-    r = rule._struct(q, context_lens.shape[0])
-    _check(lib().pa_decode_multi_scored(*a[:18], ctypes.byref(r), *a[18:]))
+    r = None if rule is None else ctypes.byref(rule._struct(q, context_lens.shape[0]))
+    _check(lib().pa_decode_multi_scored(*a[:18], r, *a[18:]))
 
 
 def pa_decode_noalloc(out, q, k_cache, v_cache, block_tables, context_lens, scale,
