@@ -479,7 +479,19 @@ pa_status pa_decode_partitions_fp8(void* out, const void* q, const void* k_cache
  * (f32 / f16 / bf16), partitions and workspace as pa_decode_fp8 (partition_size
  * 0: a length of its own, never more partitions than the default's).  A scale
  * outside [2^-40, 2^80] is read as the nearer bound, so one of an all-zero
- * block may hold 0.  Precision as pa_decode_fp8.
+ * block may hold 0.
+ * Precision: products and sums in fp32 (the sum of the weights too), the result
+ * rounded to dtype once; the weights P that multiply V are
+ *   f32 queries                          fp32
+ *   head size 128, bf16 queries, and f16 queries with two or more heads per kv
+ *   head or max_context_len > 1024 (the tensor cores; partition a multiple of
+ *   128): two (bf16) or three (f16) E4M3 terms, within 2^-8 or 2^-12 of P, and
+ *   where P is small beside the largest product of a weight and its value scale,
+ *   within 2^-16 of that product; the query as two or three terms, within 2^-17
+ *   of its largest component
+ *   else f16 queries with one or two heads per kv head   rounded to f16 (2^-11)
+ *   else                                                 fp32
+ * (pa_decode_fp8 keeps bf16 queries' P in fp32 at one and two heads.)
  *
  * pa_copy_blocks_fp8_block / pa_swap_blocks_fp8_block: pa_copy_blocks /
  * pa_swap_blocks of codes and scales in one launch (copy-on-write, forks,
@@ -532,6 +544,10 @@ pa_status pa_swap_blocks_fp8_block(void* dst_k_cache, void* dst_v_cache, float* 
  * Inf included -- with one exception: in pa_decode_multi_scored a V element that
  * is not finite, between the first and the last position that some query token
  * of its sequence sees, may reach all the sequence's query tokens.
+ *
+ * Precision: as pa_decode.  On the tensor cores (pa_decode_scored where pa_decode
+ * runs there; pa_decode_multi_scored always, as pa_decode_multi) the weights P are
+ * rounded to dtype before they multiply V, their sum is taken in fp32.
  */
 typedef struct pa_score_rule {
   float softcap;               /* 0: no cap; else > 0, at most 2^20; a capped score is off by
@@ -540,9 +556,10 @@ typedef struct pa_score_rule {
   const float* alibi_slopes;   /* [Hq] float32 (device), or NULL */
   const int32_t* key_starts;   /* [query rows] int32 (device): the first position of the row's
                                   document (packed documents), or NULL */
-  const int32_t* prefix_lens;  /* [num_seqs] int32 (device): leading tokens that every token of
-                                  the sequence sees (a prefix attended in both directions),
-                                  or NULL; without effect on a single query */
+  const int32_t* prefix_lens;  /* [num_seqs] int32 (device): leading tokens that query tokens
+                                  before their end see as well (a prefix attended in both
+                                  directions; a window or a document start hides them all the
+                                  same), or NULL; without effect on a single query */
 } pa_score_rule;
 
 /*

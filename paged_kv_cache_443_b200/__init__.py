@@ -587,7 +587,8 @@ class ScoreRule:
     softcap c > 0: c * tanh(s / c); alibi_slopes float32 [Hq]: - slope * |pos - j|;
     window w > 0: only the last w positions; key_starts int32 [query rows]: the
     first position of the row's document; prefix_lens int32 [B]: leading tokens
-    that every query token of the sequence sees.  Tensors on the queries' device."""
+    that query tokens before their end see as well (unless window or key_starts
+    hide them).  Tensors on the queries' device."""
 
     def __init__(self, softcap: float = 0.0, window: int = 0, alibi_slopes=None, key_starts=None,
                  prefix_lens=None):
