@@ -66,7 +66,6 @@ static_assert(NT == 2, "TMEM holds (S, O) of two blocks");
 
 struct Params {
   void* out;
-  const void* q;
   const int32_t* block_tables;
   const int32_t* context_lens;
   const int32_t* query_start;
@@ -601,7 +600,6 @@ cudaError_t launch_t(const MqArgs& a, unsigned int* status, cudaStream_t stream)
   if (!make_tmap(&mq, a.q, 4, qdims, qstrides, qbox, a.dtype)) return cudaErrorInvalidValue;
   Params p;
   p.out = a.out;
-  p.q = a.q;
   p.block_tables = a.block_tables;
   p.context_lens = a.context_lens;
   p.query_start = a.query_start;
