@@ -34,8 +34,9 @@ def _filled(shape, fill: float, dtype: torch.dtype, device) -> torch.Tensor:
 
 
 def _other(stream):
-    """`stream` (a torch stream or a raw handle, as the calls take it) as a torch
-    stream; None where it is the current one, or not given."""
+    """`stream` (a torch stream, an object with its handle as `cuda_stream`, or a raw
+    handle: what the calls take) as a torch stream; None where it is the current
+    one, or not given."""
     if stream is None:
         return None
     handle = getattr(stream, "cuda_stream", stream)
@@ -45,7 +46,7 @@ def _other(stream):
         return None
     if handle == 0:
         return torch.cuda.default_stream()
-    if hasattr(stream, "cuda_stream"):
+    if isinstance(stream, torch.Stream):
         return stream
     return torch.cuda.ExternalStream(handle, device=torch.cuda.current_device())
 

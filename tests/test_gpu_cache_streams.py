@@ -25,9 +25,11 @@ def clean_status():
 class Busy:
     """Calls on a stream that is behind the host by a tenth of a second each."""
 
-    def __init__(self, raw):
+    def __init__(self, kind):
         self.side = torch.cuda.Stream()
-        self.given = self.side.cuda_stream if raw else self.side
+        handle = self.side.cuda_stream
+        self.given = {"stream": self.side, "handle": handle,
+                      "wrapper": type("Wrapper", (), {"cuda_stream": handle})()}[kind]
         self.filled = []
 
     def __call__(self, call, *nbytes):
@@ -49,8 +51,8 @@ def draw(gen, *shape):
     return torch.randn(*shape, generator=gen).to(torch.bfloat16)
 
 
-@pytest.mark.parametrize("raw", [False, True])
-def test_attention_on_another_stream(raw):
+@pytest.mark.parametrize("kind", ["stream", "handle", "wrapper"])
+def test_attention_on_another_stream(kind):
     gen = torch.Generator().manual_seed(21)
     lens, counts = [1300, 900], [3, 5]
     kv = PagedKVCache(160, BS, HEADS, DIM, torch.bfloat16)
@@ -70,7 +72,7 @@ def test_attention_on_another_stream(raw):
     ws_one = pk.pa_decode_workspace_bytes(2, HEADS * GROUP, DIM, longest)
     assert ws_multi and ws_one
     torch.cuda.synchronize()
-    busy = Busy(raw)
+    busy = Busy(kind)
     got = []
     for r in (None, rule):
         got.append(busy(lambda s, r=r: kv.decode_multi(dq, table, length, start, longest, 5, SCALE,
@@ -89,8 +91,8 @@ def test_attention_on_another_stream(raw):
             assert worst(out[rows[b]], want, tol) <= 1, (i, b)
 
 
-@pytest.mark.parametrize("raw", [False, True])
-def test_block_scaled_cache_on_another_stream(raw):
+@pytest.mark.parametrize("kind", ["stream", "handle", "wrapper"])
+def test_block_scaled_cache_on_another_stream(kind):
     """Append, copy-on-write, swap out and in, decode: uploaded slots and pairs."""
     gen = torch.Generator().manual_seed(22)
     kv = PagedKVCache(200, BS, HEADS, DIM, torch.float8_e4m3fn, block_scales=True)
@@ -104,7 +106,7 @@ def test_block_scaled_cache_on_another_stream(raw):
     dq = q.cuda()
     kv.add(0)
     torch.cuda.synchronize()
-    busy = Busy(raw)
+    busy = Busy(kind)
 
     def store(seqs, counts, i):
         n = sum(counts)
